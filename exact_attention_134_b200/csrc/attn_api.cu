@@ -50,6 +50,13 @@ int* device_status_ptr() {
   if (!g_encode) return nullptr;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  // A thread that made no CUDA call yet (autograd's, on its first node) has no
+  // current context, which the tensor-map encoder needs.
+  static thread_local int bound = -1;
+  if (bound != dev) {
+    if (cudaSetDevice(dev) != cudaSuccess) return nullptr;
+    bound = dev;
+  }
   std::lock_guard<std::mutex> lock(g_dev_mutex);
   if (!g_status_ptr[dev]) {
     void* ptr = nullptr;
