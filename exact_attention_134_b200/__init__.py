@@ -10,6 +10,10 @@ missing or cannot run, the call raises.
     o, lse = attn_fwd(q, k, v, causal=True)          # bf16 [B,H,N,d] on cuda
     dq, dk, dv = attn_bwd(q, k, v, o, lse, do, causal=True)
     o = attention(q, k, v, causal=True); o.backward(do)  # torch autograd
+
+Before it and beside it: norm_rope.py (per-head norm and rotation of queries and
+keys), kv4.py (the paged 4-bit key/value cache and attention over it),
+kv4_pages.py (the host's bookkeeping of its pages).
 """
 from __future__ import annotations
 
@@ -42,6 +46,7 @@ _lib = None
 _lock = threading.Lock()
 
 _c_int, _c_float, _vp, _sz = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+_ll = ctypes.c_longlong
 _SIGNATURES = {
     "attn_fwd": (_c_int, [_vp, _vp, _vp, _vp, _vp] + [_c_int] * 7 + [_c_float, _vp]),
     "attn_fwd_varlen": (_c_int, [_vp] * 7 + [_c_int] * 8 + [_c_float, _vp]),
@@ -65,6 +70,16 @@ _SIGNATURES = {
     "attn_bwd": (_c_int, [_vp] * 9 + [_c_int] * 7 + [_c_float, _vp, _sz, _vp]),
     "attn_bwd_varlen_workspace_size": (_sz, [_c_int] * 4),
     "attn_bwd_varlen": (_c_int, [_vp] * 11 + [_c_int] * 9 + [_c_float, _vp, _sz, _vp]),
+    "attn_qk_norm_rope": (_c_int, [_vp] * 7 + [_c_int, _vp, _ll, _ll, _vp, _vp] + [_c_int] * 8 + [_c_float, _vp]),
+    "attn_qk_norm_rope_bwd_workspace_size": (_sz, [_c_int] * 5),
+    "attn_qk_norm_rope_bwd": (_c_int, [_vp] * 9 + [_c_int, _vp, _vp, _vp, _ll, _ll, _vp, _vp] + [_c_int] * 8 +
+                              [_c_float, _vp, _sz, _vp]),
+    "attn_kv4_page_bytes": (_sz, [_c_int] * 3),
+    "attn_kv4_append": (_c_int, [_vp, _vp] + [_ll] * 4 + [_vp] * 4 + [_c_int] * 7 + [_vp]),
+    "attn_kv4_gather": (_c_int, [_vp] * 4 + [_c_int] * 7 + [_vp] * 3),
+    "attn_kv4_copy_pages": (_c_int, [_vp, _c_int, _c_int, _sz, _vp, _vp, _c_int, _vp]),
+    "attn_fwd_kv4_workspace_size": (_sz, [_c_int] * 4),
+    "attn_fwd_kv4": (_c_int, [_vp] * 7 + [_c_int] * 10 + [_c_float, _vp, _sz, _vp]),
     "attn_selftest_wait_timeout": (_c_int, [_c_int, _vp]),
     "attn_get_status": (_c_int, [_vp]),
     "attn_get_status_ex": (_c_int, [_vp, ctypes.POINTER(_c_int)]),
@@ -105,6 +120,25 @@ def _check(status: int, what: str):
 def _stream_handle(device=None) -> int:
     import torch
     return torch.cuda.current_stream(device).cuda_stream
+
+
+class _current_device:
+    """Makes `device` the current one for a call (the library launches there)."""
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        import torch
+        here = torch.cuda.current_device()
+        self.back = None if here == self.device.index else here
+        if self.back is not None:
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            import torch
+            torch.cuda.set_device(self.back)
 
 
 def _shape_args(q, k, v):
@@ -562,3 +596,10 @@ def set_timeout_ms(ms: int):
 
 def version() -> int:
     return int(lib().attn_version())
+
+
+# Queries and keys before attention, and the 4-bit cache.
+from .kv4 import (attn_fwd_kv4, fwd_kv4_workspace_size, kv4_alloc, kv4_append, kv4_copy_pages,  # noqa: E402
+                  kv4_gather, kv4_page_bytes)
+from .kv4_pages import KV4Pages, OutOfPages, page_pairs  # noqa: E402
+from .norm_rope import norm_rope, qk_norm_rope, qk_norm_rope_bwd  # noqa: E402

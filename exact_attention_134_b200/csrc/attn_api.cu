@@ -530,6 +530,9 @@ namespace attn_sm100 {
 
 attn_status_t cuda_error_status(cudaError_t e) { return cuda_status(e); }
 
+int* device_status_word() { return device_status_ptr(); }
+unsigned long long wait_budget_ns() { return (unsigned long long)g_timeout_ns.load(); }
+
 // Internal: the argument checks of attn_fwd / attn_fwd_q8.
 attn_status_t validate_fwd_args(const void* q, const void* k, const void* v, const void* o,
                                 const void* lse, int B, int Hq, int Hkv, int Nq, int Nkv, int d,

@@ -172,6 +172,11 @@ cudaError_t launch_bwd(const BwdLaunch& L, int d, cudaStream_t stream);
 // (per calling thread) and returns ATTN_ERR_CUDA.
 attn_status_t cuda_error_status(cudaError_t e);
 
+// The current device's status word (nullptr if it cannot be had) and the
+// budget of a pipeline wait.
+int* device_status_word();
+unsigned long long wait_budget_ns();
+
 attn_status_t validate_fwd_args(const void* q, const void* k, const void* v, const void* o,
                                 const void* lse, int B, int Hq, int Hkv, int Nq, int Nkv, int d,
                                 int causal, float scale);
@@ -200,5 +205,12 @@ cudaError_t launch_merge(const float* o_parts, const float* lse_parts, int num_p
 cudaError_t launch_fwd_d256(const CUtensorMap& tk, const CUtensorMap& tv, const void* q,
                             const FwdParams& p, cudaStream_t stream);
 int fwd_rows_per_cta_d256();
+
+// Checks the arguments that every entry point of the 4-bit cache shares and
+// fills in the pool's description (kv4_format.cuh).
+struct Kv4Pool;
+attn_status_t kv4_pool_params(Kv4Pool* c, const void* pool, const int* page_table, const int* seq_lens,
+                              const int* cu, int num_seqs, int max_pages, int num_pages, int page_size,
+                              int total, int Hkv, int d);
 
 }  // namespace attn_sm100

@@ -1,0 +1,779 @@
+// attn_kv4_sm100.cu — attention over the paged 4-bit cache (kv4_format.cuh)
+// for a few query tokens a sequence, and the merge of its split results.
+//
+//   S_ij = scale * sum_g (s_jg * sum_{c in g} q_ic code_jc + lo_jg * sum_{c in g} q_ic)
+//   O_i  = sum_j p_ij (lo_jg + s_jg code_jc) / sum_j p_ij,  p_ij = 2^(S_ij log2(e) - R_i)
+// so the codes themselves are the operands of the matrix instructions and the
+// keys and values are never rounded: scale and minimum come in afterwards (K,
+// on the fp32 sums of a group) or before (V: p * s, one operand a group; the
+// minimum times p is one more, small product).
+//
+// Operands. A code in the low bits of a 16-bit half is the fp16 subnormal
+// code * 2^-24, exact in the tensor core, and one 4 bits up is 16 times that:
+// a word of 8 codes becomes four operand registers with four ANDs and a shift.
+// The scores are taken as S^T = K Q^T (16 keys x 8 query rows an instruction)
+// and the output as O^T = V^T P^T: with one token and at most 8 query heads a
+// kv head, 8 columns hold the rows, where 64 or 128 rows of a tcgen05 tile
+// would be filled up with zeros, and operands go from the dequantised register
+// straight into the instruction; tcgen05 would need them written to shared or
+// tensor memory first. Q is scaled by a power of two a row into fp16's range;
+// P^T = p * s is fp16 as well, against a reference that follows the row's
+// maximum and the scales: p * s < 2^15.
+//
+// HBM-bound: 1.25 d bytes a cached token and kv head for K and V, against some
+// 260 warp instructions a record of 16 tokens (20 d = 2560 bytes at d = 128:
+// 111 clocks of an SM's share of the memory rate, 444 issue slots).
+//
+// Work. A unit is one record of one block of query rows; the units of all
+// sequences, kv heads and row blocks form one list, cut into equal ranges, one
+// per CTA, whatever the lengths. The warps of a CTA take the records of a
+// segment (the part of one row block in its range) in turn, each with its own
+// ring of bulk copies (one copy a record) and its own softmax state; they are
+// joined in shared memory at the segment's end. A row block within one range
+// is written out there; one cut by a range's border leaves fp32 partial
+// results, which the merge kernel joins.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "attn_internal.h"
+#include "kv4_format.cuh"
+#include "sm100_ptx.cuh"
+
+namespace attn_sm100 {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kNone = -3.0e38f;  // reference of a row that has seen no key
+constexpr int kMinScale = -64;       // smaller scales count as 2^-64: p stays below 2^79
+constexpr float kHead = 8.0f;      // log2 of p * s at the reference: 2^7 of room before the next rescale
+
+struct Kv4Params {
+  Kv4Pool c;
+  const uint16_t* q;   // bf16 [total, Hq, d]
+  uint16_t* o;         // bf16 [total, Hq, d]
+  float* lse;          // fp32 [Hq, total]
+  float* part_o;       // [2 * CTAs][columns][d]: partial sums of a range's first and last row block
+  float2* part_rl;     // [2 * CTAs][columns]: their reference and exponential sum
+  int4* split;         // [CTAs][2]: what the merge does at the range's first border
+  int* status;
+  int Hq, group;
+  int causal;
+  int min_units;       // smallest range worth a CTA
+  float scale_log2;
+  unsigned long long timeout_ns;
+};
+
+template <int D, int NT>
+struct Kv4Cfg {
+  static constexpr int kWarps = (NT == 1 && D <= 128) ? 8 : 4;
+  static constexpr int kCtasPerSm = NT == 2 && D == 64 ? 3 : 2;
+  static constexpr int kStages = 3;
+  static constexpr int kCols = 8 * NT;
+  static constexpr int kRecord = kv4_record_bytes(D);
+  static constexpr int kRing = kWarps * kStages * kRecord;
+  static constexpr int kJoin = kWarps * kCols * D * 4;        // fp32 O of every warp
+  static constexpr int kRl = 2 * kWarps * kCols * 8;          // (reference, sum), two segments
+  static constexpr int kBars = kWarps * kStages * 8;
+  static constexpr int kSmemBytes = kRing + kJoin + kRl + kBars + 16;
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %5}, {%7, %8}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1));
+}
+
+// 8 x 8 transposition of 16-bit values over the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// N consecutive words of shared memory, in the widest loads their alignment allows.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t addr) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "r"(addr + 4 * i));
+  } else if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[i]), "=r"(w[i + 1]) : "r"(addr + 4 * i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[i]) : "r"(addr + 4 * i));
+  }
+}
+
+__device__ __forceinline__ void lds_pair(uint32_t& a, uint32_t& b, uint32_t addr) {
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
+}
+
+__device__ __forceinline__ uint32_t lds_word(uint32_t addr) {
+  uint32_t a;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a) : "r"(addr));
+  return a;
+}
+
+// A sequence's part in the list of units: `blocks` row blocks for each kv
+// head, `units` for each of those (one per record; one also for an empty
+// cache, so that its rows get their result).
+struct SeqWork {
+  int first, n, len, blocks, units;
+};
+template <int COLS>
+__device__ __forceinline__ SeqWork seq_work(const Kv4Params& p, int b) {
+  SeqWork s;
+  kv4_rows(p.c, b, s.first, s.n);
+  s.len = kv4_len(p.c, b);
+  s.blocks = (int)(((long long)s.n * p.group + COLS - 1) / COLS);
+  s.units = max(1, (s.len + kKv4Tile - 1) / kKv4Tile);
+  return s;
+}
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// One segment: the units [t0, t1) of row block rb of kv head h of sequence b.
+struct Segment {
+  int b, h, rb, t0, t1;
+  SeqWork s;
+};
+
+// Finds the segment of the list that holds unit `u` (the whole warp takes
+// part). False if the list ends before it.
+template <int COLS>
+__device__ __forceinline__ bool find_segment(const Kv4Params& p, long long u, Segment& g) {
+  const int lane = threadIdx.x & 31;
+  long long base = 0;
+  for (int b0 = 0; b0 < p.c.num_seqs; b0 += 32) {
+    long long mine = 0;
+    if (b0 + lane < p.c.num_seqs) {
+      const SeqWork s = seq_work<COLS>(p, b0 + lane);
+      mine = (long long)s.blocks * p.c.Hkv * s.units;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned past = __ballot_sync(kFull, base + incl > u);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      g.b = b0 + l;
+      g.s = seq_work<COLS>(p, g.b);
+      const long long in = u - base - __shfl_sync(kFull, incl - mine, l);
+      const long long which = in / g.s.units;
+      g.t0 = (int)(in % g.s.units);
+      g.h = (int)(which / g.s.blocks);
+      g.rb = (int)(which % g.s.blocks);
+      return true;
+    }
+    base += __shfl_sync(kFull, incl, 31);
+  }
+  return false;
+}
+
+// Steps to the next segment of the list (its start; t1 is the caller's). False at the end.
+template <int COLS>
+__device__ __forceinline__ bool next_segment(const Kv4Params& p, Segment& g) {
+  g.t0 = 0;
+  if (++g.rb < g.s.blocks) return true;
+  g.rb = 0;
+  if (++g.h < p.c.Hkv) return true;
+  g.h = 0;
+  while (++g.b < p.c.num_seqs) {
+    g.s = seq_work<COLS>(p, g.b);
+    if (g.s.blocks > 0) return true;
+  }
+  return false;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCtasPerSm)
+    attn_kv4_kernel(const __grid_constant__ Kv4Params p) {
+  using C = Kv4Cfg<D, NT>;
+  constexpr int W = C::kWarps, S = C::kStages, G = D / 32, COLS = C::kCols;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* const join = reinterpret_cast<float*>(smem + C::kRing);
+  float2* const rl = reinterpret_cast<float2*>(smem + C::kRing + C::kJoin);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + C::kRing + C::kJoin + C::kRl + C::kBars);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
+  const uint32_t ring = smem_addr(smem) + warp * S * C::kRecord;
+  const uint32_t bars = smem_addr(smem + C::kRing + C::kJoin + C::kRl) + warp * S * 8;
+
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < S; ++i) mbar_init(bars + 8 * i, 1);
+    fence_mbarrier_init();
+  }
+  if (threadIdx.x == 0) *abort_flag = 0;
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // this CTA's range of the list
+  long long total = 0;
+  for (int b0 = 0; b0 < p.c.num_seqs; b0 += 32) {
+    if (b0 + lane < p.c.num_seqs) {
+      const SeqWork s = seq_work<COLS>(p, b0 + lane);
+      total += (long long)s.blocks * p.c.Hkv * s.units;
+    }
+  }
+  total = warp_sum(total);
+  const long long ctas = max(1LL, min((long long)gridDim.x, total / p.min_units));
+  const long long begin = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
+  Segment seg;
+  const bool any = blockIdx.x < ctas && begin < end && find_segment<COLS>(p, begin, seg);
+  if (threadIdx.x == 0) {
+    // a row block cut by this range's first border, and by none before: what the merge joins
+    int4 a = make_int4(0, 0, 0, 0), z = a;
+    if (any && seg.t0 > 0) {
+      const long long u0 = begin - seg.t0, u1 = u0 + seg.s.units - 1;
+      const int c0 = (int)(((u0 + 1) * ctas - 1) / total), c1 = (int)(((u1 + 1) * ctas - 1) / total);
+      if (c0 + 1 == (int)blockIdx.x) {
+        a = make_int4(1, c0, c1, seg.h);
+        z = make_int4(seg.rb, seg.s.first, seg.s.n, 0);
+      }
+    }
+    p.split[2 * blockIdx.x] = a;
+    p.split[2 * blockIdx.x + 1] = z;
+  }
+  if (!any) return;
+
+  // ---- the ring: this warp's records, over all segments of the range
+  Segment pf = seg;
+  long long pf_left = end - begin;
+  pf.t1 = (int)min((long long)pf.s.units, pf.t0 + pf_left);
+  int pf_k = 0;           // next record of the warp in pf: unit t0 + warp + W * pf_k
+  int pf_pages = 0;       // page of record (pf_k / 32) * 32 + lane
+  bool pf_more = true;
+  unsigned issued = 0, taken = 0;
+  uint32_t bad = 0;       // bit s: the record of stage s is on no page of the pool
+
+  auto records = [&](const Segment& g) {  // of this warp in segment g
+    const int e = min(g.t1, (g.s.len + kKv4Tile - 1) / kKv4Tile);
+    return max(0, (e - g.t0 - warp + W - 1) / W);
+  };
+  auto issue = [&]() {
+    while (pf_more && pf_k >= records(pf)) {
+      pf_left -= pf.t1 - pf.t0;
+      pf_more = pf_left > 0 && next_segment<COLS>(p, pf);
+      if (pf_more) pf.t1 = (int)min((long long)pf.s.units, pf_left);
+      pf_k = 0;
+    }
+    if (!pf_more) return;
+    if ((pf_k & 31) == 0) {
+      const int t = pf.t0 + warp + W * (pf_k + lane);
+      pf_pages = t < pf.t1 && t * kKv4Tile < pf.s.len
+                     ? __ldg(p.c.table + (size_t)pf.b * p.c.max_pages + (t >> p.c.tiles_log2))
+                     : -1;
+    }
+    const int page = __shfl_sync(kFull, pf_pages, pf_k & 31);
+    const int t = pf.t0 + warp + W * pf_k;
+    const int st = issued % S;
+    const bool ok = page >= 0 && page < p.c.num_pages;
+    bad = ok ? bad & ~(1u << st) : bad | (1u << st);
+    if (lane == 0) {
+      if (ok) {
+        mbar_arrive_expect_tx(bars + 8 * st, C::kRecord);
+        bulk_load(ring + st * C::kRecord,
+                  p.c.data + kv4_record(p.c, page, pf.h, t & ((1 << p.c.tiles_log2) - 1), D), C::kRecord, bars + 8 * st);
+      } else {
+        mbar_arrive(bars + 8 * st);
+        kv4_bad_page(p.status, 0x500);
+      }
+    }
+    ++issued;
+    ++pf_k;
+  };
+#pragma unroll 1
+  for (int i = 0; i < S; ++i) issue();
+
+  long long left = end - begin;
+  seg.t1 = (int)min((long long)seg.s.units, seg.t0 + left);
+  bool ok = true;
+  int turn = 0;  // parity of the segment, for rl
+  while (true) {
+    // ---- query rows of the segment, as operands
+    uint32_t qf[NT][G][4];
+    float qsum[NT][G][2], fac[NT][2];
+    int limit[NT][2];  // last key that the lane's two columns see
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = seg.rb * COLS + nt * 8 + g8;
+      const bool live = row < seg.s.n * p.group;
+      const int tok = seg.s.first + row / p.group;
+      const uint16_t* const src = p.q + ((size_t)tok * p.Hq + seg.h * p.group + row % p.group) * D + 8 * t4;
+      uint4 raw[G];
+      uint32_t top = 0;
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        raw[gr] = live ? __ldg(reinterpret_cast<const uint4*>(src + 32 * gr)) : make_uint4(0, 0, 0, 0);
+        top = max(max(top, max(raw[gr].x & 0x7fffu, (raw[gr].x >> 16) & 0x7fffu)),
+                  max(raw[gr].y & 0x7fffu, (raw[gr].y >> 16) & 0x7fffu));
+        top = max(max(top, max(raw[gr].z & 0x7fffu, (raw[gr].z >> 16) & 0x7fffu)),
+                  max(raw[gr].w & 0x7fffu, (raw[gr].w >> 16) & 0x7fffu));
+      }
+      top = max(top, __shfl_xor_sync(kFull, top, 1));
+      top = max(top, __shfl_xor_sync(kFull, top, 2));
+      // the row's largest value into [2^13, 2^14): a sixteenth of it, for the
+      // codes that stand 4 bits up, still is a normal number down to 2^-24 of it
+      const int k = min(max(13 - ((int)(top >> 7) - 127), -90), 100);
+      const float up = __uint_as_float((uint32_t)(k + 127) << 23);
+      float sum[G];
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        const uint32_t w[4] = {raw[gr].x, raw[gr].y, raw[gr].z, raw[gr].w};
+        float f[8];
+        sum[gr] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          f[i] = (i % 2 ? hi16(w[i / 2]) : lo16(w[i / 2])) * up;
+          sum[gr] += f[i];
+        }
+        // codes i and i + 4 share a register; 1, 3, 5, 7 stand 4 bits up
+        qf[nt][gr][0] = pack_f16x2(f[0], f[4]);
+        qf[nt][gr][1] = pack_f16x2(f[1] * 0.0625f, f[5] * 0.0625f);
+        qf[nt][gr][2] = pack_f16x2(f[2], f[6]);
+        qf[nt][gr][3] = pack_f16x2(f[3] * 0.0625f, f[7] * 0.0625f);
+        sum[gr] += __shfl_xor_sync(kFull, sum[gr], 1);
+        sum[gr] += __shfl_xor_sync(kFull, sum[gr], 2);
+      }
+      const float back = p.scale_log2 * __uint_as_float((uint32_t)(24 - k + 127) << 23);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {  // the lane's columns 2 t4 + j
+        const int from = 4 * (2 * t4 + j);
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) qsum[nt][gr][j] = __shfl_sync(kFull, sum[gr], from) * 5.9604644775390625e-8f;  // 2^-24
+        fac[nt][j] = __shfl_sync(kFull, back, from);
+        const int r = seg.rb * COLS + nt * 8 + 2 * t4 + j;
+        limit[nt][j] = p.causal ? seg.s.len - seg.s.n + min(r / p.group, seg.s.n - 1) : seg.s.len - 1;
+      }
+    }
+    // every key up to this one is seen by all rows of the block
+    const int all_see = p.causal ? seg.s.len - seg.s.n + seg.rb * COLS / p.group : seg.s.len - 1;
+
+    float o[NT][2 * G][4], omin[NT][4], ref[NT][2], sum[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int m = 0; m < 2 * G; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nt][m][i] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) omin[nt][i] = 0.0f;
+      ref[nt][0] = ref[nt][1] = kNone;
+      sum[nt][0] = sum[nt][1] = 0.0f;
+    }
+
+    const int mine = records(seg);
+#pragma unroll 1
+    for (int k = 0; k < mine && ok; ++k) {
+      const int st = taken % S;
+      ok = __all_sync(kFull, bounded_wait(bars + 8 * st, (taken / S) & 1u, abort_flag, p.timeout_ns));
+      if (!ok) break;
+      ++taken;
+      if (bad >> st & 1u) {
+        issue();
+        continue;
+      }
+      const int key = (seg.t0 + warp + W * k) * kKv4Tile + g8;  // the lane's keys: key and key + 8
+      const bool edge = key - g8 + kKv4Tile - 1 > all_see;
+      const uint32_t rec = ring + st * C::kRecord;
+
+      // ---- scores
+      float x[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[nt][i] = 0.0f;
+      {
+        uint32_t ks[G], kl[G];
+        lds_words<G>(ks, rec + 16 * D + g8 * G * 4);
+        lds_words<G>(kl, rec + 17 * D + g8 * G * 4);
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+          uint32_t w0, w1;
+          lds_pair(w0, w1, rec + gr * 256 + lane * 8);
+          const float s0 = lo16(ks[gr]), s1 = hi16(ks[gr]), m0 = lo16(kl[gr]), m1 = hi16(kl[gr]);
+          float acc[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
+            mma_f16(acc[nt], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, qf[nt][gr][0],
+                    qf[nt][gr][1]);
+            mma_f16(acc[nt], (w0 >> 8) & 0x000f000fu, (w1 >> 8) & 0x000f000fu, (w0 >> 8) & 0x00f000f0u,
+                    (w1 >> 8) & 0x00f000f0u, qf[nt][gr][2], qf[nt][gr][3]);
+            x[nt][0] = fmaf(m0, qsum[nt][gr][0], fmaf(s0, acc[nt][0], x[nt][0]));
+            x[nt][1] = fmaf(m0, qsum[nt][gr][1], fmaf(s0, acc[nt][1], x[nt][1]));
+            x[nt][2] = fmaf(m1, qsum[nt][gr][0], fmaf(s1, acc[nt][2], x[nt][2]));
+            x[nt][3] = fmaf(m1, qsum[nt][gr][1], fmaf(s1, acc[nt][3], x[nt][3]));
+          }
+        }
+      }
+      // ---- the rest of the record, then its stage is free
+      uint32_t vw[G][2], vs[G], vm[2];
+      lds_words<G>(vs, rec + 18 * D + g8 * G * 4);
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) lds_pair(vw[gr][0], vw[gr][1], rec + 8 * D + gr * 256 + lane * 8);
+      vm[0] = g8 < G ? lds_word(rec + 19 * D + g8 * 32 + t4 * 4) : 0u;
+      vm[1] = g8 < G ? lds_word(rec + 19 * D + g8 * 32 + 16 + t4 * 4) : 0u;
+      __syncwarp();
+      issue();
+
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[nt][i] *= fac[nt][i & 1];
+      if (edge) {
+        // keys behind the cached ones hold anything: no scale or minimum of
+        // theirs counts; keys that a row does not see get -inf
+        const uint32_t keep = (key < seg.s.len ? 0x0000ffffu : 0u) | (key + 8 < seg.s.len ? 0xffff0000u : 0u);
+        const int pair = key - g8 + 2 * t4;
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) vs[gr] &= keep;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          vm[i] &= (pair + 8 * i < seg.s.len ? 0x0000ffffu : 0u) | (pair + 8 * i + 1 < seg.s.len ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (key + (i & 2) * 4 > limit[nt][i & 1]) x[nt][i] = -INFINITY;
+      }
+      // ---- the largest V scale of the record is below 2^e; so is a 2^-48th of
+      // its minima, whose products with p would overflow behind smaller ones
+      // (and need no codes: the minima's weights hold 16 bits)
+      uint32_t top = 0, vtop = __vmaxu2(vm[0] & 0x7fff7fffu, vm[1] & 0x7fff7fffu);
+      vtop = max(vtop & 0xffffu, vtop >> 16);
+      vtop = vtop > (48u << 7) ? vtop - (48u << 7) : 0u;
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) top = __vmaxu2(top, vs[gr] & 0x7fff7fffu);
+      top = __reduce_max_sync(kFull, max(max(top & 0xffffu, top >> 16), vtop));
+      if (top >= 0x7f80u) {  // NaN groups: of no weight in the choice of the reference
+        top = vtop;
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+          const uint32_t a = vs[gr] & 0x7fffu, b = (vs[gr] >> 16) & 0x7fffu;
+          top = max(top, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
+        }
+        top = __reduce_max_sync(kFull, top);
+      }
+      const float e = (float)max((int)(top >> 7) - 126, kMinScale);
+      // ---- a new reference where p * s would pass 2^15
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) over |= fmaxf(x[nt][j], x[nt][2 + j]) - ref[nt][j] > 15.0f - e;
+      if (__any_sync(kFull, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float m = fmaxf(x[nt][j], x[nt][2 + j]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+            const float next = fmaxf(ref[nt][j], m + (e - kHead));
+            const float f = ex2_approx(ref[nt][j] - next);
+            ref[nt][j] = next;
+            sum[nt][j] *= f;
+#pragma unroll
+            for (int q = 0; q < 2 * G; ++q) {
+              o[nt][q][j] *= f;
+              o[nt][q][2 + j] *= f;
+            }
+            omin[nt][j] *= f;
+          }
+      }
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float pr[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pr[i] = ex2_approx(x[nt][i] - ref[nt][i & 1]);
+        sum[nt][0] += pr[0] + pr[2];
+        sum[nt][1] += pr[1] + pr[3];
+        {
+          // the minimum's weights in two bf16 steps (16 bits): the minimum and
+          // the codes' part cancel, so a single one would show in the result
+          const uint32_t h0 = __byte_perm(__float_as_uint(pr[0]), __float_as_uint(pr[1]), 0x7632);
+          const uint32_t h1 = __byte_perm(__float_as_uint(pr[2]), __float_as_uint(pr[3]), 0x7632);
+          const uint32_t l0 = pack_bf16x2(pr[0] - lo16(h0), pr[1] - hi16(h0));
+          const uint32_t l1 = pack_bf16x2(pr[2] - lo16(h1), pr[3] - hi16(h1));
+          mma_bf16(omin[nt], vm[0], vm[1], transpose8(h0), transpose8(h1));
+          mma_bf16(omin[nt], vm[0], vm[1], transpose8(l0), transpose8(l1));
+        }
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+          const float s0 = lo16(vs[gr]), s1 = hi16(vs[gr]);
+          float w[4] = {pr[0] * s0, pr[1] * s0, pr[2] * s1, pr[3] * s1};
+          if (edge) {  // a NaN group reaches only the rows that see its key
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (x[nt][i] == -INFINITY) w[i] = 0.0f;
+          }
+          const uint32_t b0 = transpose8(pack_f16x2(w[0], w[1])), b1 = transpose8(pack_f16x2(w[2], w[3]));
+          const uint32_t a = vw[gr][0], b = vw[gr][1];
+          mma_f16(o[nt][2 * gr], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u, b0, b1);
+          mma_f16(o[nt][2 * gr + 1], (a >> 8) & 0x000f000fu, (a >> 8) & 0x00f000f0u, (b >> 8) & 0x000f000fu,
+                  (b >> 8) & 0x00f000f0u, b0, b1);
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      if (atomicCAS(p.status, 0, ATTN_ERR_TIMEOUT) == 0) p.status[1] = 0x501;
+    }
+
+    // ---- join the warps
+    float2* const my_rl = rl + turn * W * COLS;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) sum[nt][j] += __shfl_xor_sync(kFull, sum[nt][j], d);
+        if (g8 == 0) my_rl[warp * COLS + nt * 8 + 2 * t4 + j] = make_float2(ref[nt][j], sum[nt][j]);
+      }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int col = nt * 8 + 2 * t4 + j;
+        float top = my_rl[col].x;
+#pragma unroll
+        for (int w = 1; w < W; ++w) top = fmaxf(top, my_rl[w * COLS + col].x);
+        const float f = ex2_approx(ref[nt][j] - top);
+        const float f0 = f * 16777216.0f, f1 = f * 1048576.0f;  // 2^24, and a sixteenth of it
+        float* const to = join + (warp * COLS + col) * D + 4 * g8;
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+          const float lo = f * __shfl_sync(kFull, omin[nt][j], gr * 4 + t4);
+          *reinterpret_cast<float4*>(to + 32 * gr) =
+              make_float4(fmaf(f0, o[nt][2 * gr][j], lo), fmaf(f1, o[nt][2 * gr][2 + j], lo),
+                          fmaf(f0, o[nt][2 * gr + 1][j], lo), fmaf(f1, o[nt][2 * gr + 1][2 + j], lo));
+        }
+      }
+    __syncthreads();
+    const bool whole = seg.t0 == 0 && seg.t1 == seg.s.units;
+    const size_t slot = 2 * (size_t)blockIdx.x + (seg.t0 > 0 ? 0 : 1);
+    for (int i = threadIdx.x; i < COLS * (D / 4); i += W * 32) {
+      const int col = i / (D / 4), c4 = i % (D / 4);
+      const int r = seg.rb * COLS + col;
+      float top = my_rl[col].x, l = 0.0f;
+#pragma unroll
+      for (int w = 1; w < W; ++w) top = fmaxf(top, my_rl[w * COLS + col].x);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float4 v = reinterpret_cast<const float4*>(join + (w * COLS + col) * D)[c4];
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+        l += my_rl[w * COLS + col].y * ex2_approx(my_rl[w * COLS + col].x - top);
+      }
+      if (!whole) {
+        reinterpret_cast<float4*>(p.part_o + (slot * COLS + col) * D)[c4] = a;
+        if (c4 == 0) p.part_rl[slot * COLS + col] = make_float2(top, l);
+      } else if (r < seg.s.n * p.group) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int tok = seg.s.first + r / p.group, head = seg.h * p.group + r % p.group;
+        reinterpret_cast<uint2*>(p.o + ((size_t)tok * p.Hq + head) * D)[c4] =
+            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+        if (c4 == 0)
+          p.lse[(size_t)head * p.c.total + tok] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+      }
+    }
+    left -= seg.t1 - seg.t0;
+    if (left <= 0 || !next_segment<COLS>(p, seg)) break;
+    seg.t1 = (int)min((long long)seg.s.units, left);
+    turn ^= 1;
+  }
+  if (!ok) {  // its own copies in flight still land in this shared memory
+    volatile int no_abort = 0;
+    for (; taken < issued; ++taken) bounded_wait(bars + 8 * (taken % S), (taken / S) & 1u, &no_abort, p.timeout_ns);
+  }
+}
+
+// Joins the partial results of the row block that border `blockIdx.x + 1` cuts
+// first, one column (query row) a block: O = sum_c 2^(R_c - R) O_c / sum_c 2^(R_c - R) l_c.
+constexpr int kMergeSlices = 8;
+template <int D>
+__global__ void __launch_bounds__(D / 4 * kMergeSlices) attn_kv4_merge_kernel(const __grid_constant__ Kv4Params p, int cols) {
+  constexpr int T = D / 4;
+  __shared__ float4 acc[kMergeSlices][T];
+  __shared__ float tops[kMergeSlices], sums[kMergeSlices];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 a = p.split[2 * (blockIdx.x + 1)], z = p.split[2 * (blockIdx.x + 1) + 1];
+  if (a.x == 0) return;
+  const int col = blockIdx.y, r = z.x * cols + col;
+  if (r >= z.z * p.group) return;
+  const int c4 = threadIdx.x % T, slice = threadIdx.x / T;
+  // parts: the last slot of CTA a.y, then the first slots of a.y + 1 .. a.z
+  float top = kNone, l = 0.0f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = a.y + slice; c <= a.z; c += kMergeSlices) {
+    const size_t at = (size_t)(2 * c + (c == a.y ? 1 : 0)) * cols + col;
+    const float2 rl = p.part_rl[at];
+    const float4 x = reinterpret_cast<const float4*>(p.part_o + at * D)[c4];
+    const float next = fmaxf(top, rl.x), f = ex2_approx(top - next), g = ex2_approx(rl.x - next);
+    top = next;
+    l = l * f + rl.y * g;
+    v = make_float4(v.x * f + x.x * g, v.y * f + x.y * g, v.z * f + x.z * g, v.w * f + x.w * g);
+  }
+  acc[slice][c4] = v;
+  if (c4 == 0) {
+    tops[slice] = top;
+    sums[slice] = l;
+  }
+  __syncthreads();
+  if (slice != 0) return;
+#pragma unroll
+  for (int i = 1; i < kMergeSlices; ++i) top = fmaxf(top, tops[i]);
+  l = 0.0f;
+  v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kMergeSlices; ++i) {
+    const float f = ex2_approx(tops[i] - top);
+    const float4 x = acc[i][c4];
+    l += f * sums[i];
+    v = make_float4(v.x + f * x.x, v.y + f * x.y, v.z + f * x.z, v.w + f * x.w);
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int tok = z.y + r / p.group, head = a.w * p.group + r % p.group;
+  reinterpret_cast<uint2*>(p.o + ((size_t)tok * p.Hq + head) * D)[c4] =
+      make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+  if (c4 == 0) p.lse[(size_t)head * p.c.total + tok] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+}
+
+// Rows of a kv head in one pass over its records: 8 columns, or 16 where a
+// sequence has more rows (at d = 256 their accumulators do not fit).
+int row_tiles(int d, long long rows) { return d <= 128 && rows > 8 ? 2 : 1; }
+
+// Most CTAs of a launch: those that are resident at once.
+int max_ctas(int d, int nt) { return 148 * (nt == 2 && d == 64 ? 3 : 2); }
+
+struct Kv4Workspace {
+  size_t rl, split, total;
+};
+Kv4Workspace workspace(int d, int nt) {
+  const size_t slots = 2 * (size_t)max_ctas(d, nt) * 8 * nt;
+  Kv4Workspace w;
+  w.rl = slots * d * 4;
+  w.split = w.rl + slots * sizeof(float2);
+  w.total = (w.split + 2 * (size_t)max_ctas(d, nt) * sizeof(int4) + 255) / 256 * 256;
+  return w;
+}
+
+template <int D, int NT>
+cudaError_t launch_kv4(const Kv4Params& p, int ctas, cudaStream_t stream) {
+  using C = Kv4Cfg<D, NT>;
+  cudaError_t e = max_dynamic_smem_once<attn_kv4_kernel<D, NT>>(C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  attn_kv4_kernel<D, NT><<<ctas, C::kWarps * 32, C::kSmemBytes, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || ctas == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas - 1, C::kCols);
+  cfg.blockDim = dim3(D / 4 * kMergeSlices);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_kv4_merge_kernel<D>, p, C::kCols);
+}
+
+}  // namespace
+}  // namespace attn_sm100
+
+using namespace attn_sm100;
+
+extern "C" {
+
+size_t attn_fwd_kv4_workspace_size(int Hq, int Hkv, int max_seqlen_q, int d) {
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || max_seqlen_q <= 0 || (d != 64 && d != 96 && d != 128 && d != 256)) return 0;
+  return workspace(d, row_tiles(d, (long long)max_seqlen_q * (Hq / Hkv))).total;
+}
+
+attn_status_t attn_fwd_kv4(const void* q, const void* pool, const int* page_table, const int* seq_lens,
+                           const int* cu_seqlens_q, void* o, float* lse, int num_seqs, int max_pages, int num_pages,
+                           int page_size, int max_seqlen_q, int total_q, int Hq, int Hkv, int d, int causal,
+                           float scale, void* workspace_ptr, size_t workspace_bytes, void* stream) {
+  if (!q || !o || !lse || Hq <= 0 || Hkv <= 0 || Hq % Hkv || max_seqlen_q <= 0) return ATTN_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+  if (!isfinite(scale) || !(scale > 0.0f)) return ATTN_ERR_INVALID_ARG;
+  Kv4Params p;
+  const attn_status_t s = kv4_pool_params(&p.c, pool, page_table, seq_lens, cu_seqlens_q, num_seqs, max_pages,
+                                          num_pages, page_size, total_q, Hkv, d);
+  if (s != ATTN_OK) return s;
+  if (Hq > 65535) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)total_q * (Hq / Hkv) > 0x7fffff00LL) return ATTN_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(lse)) & 15u)
+    return ATTN_ERR_ALIGNMENT;
+  const int nt = row_tiles(d, (long long)max_seqlen_q * (Hq / Hkv));
+  const Kv4Workspace w = workspace(d, nt);
+  if (!workspace_ptr || (reinterpret_cast<uintptr_t>(workspace_ptr) & 15u) || workspace_bytes < w.total)
+    return ATTN_ERR_WORKSPACE;
+  p.status = device_status_word();
+  if (!p.status) return ATTN_ERR_CUDA;
+  uint8_t* const ws = static_cast<uint8_t*>(workspace_ptr);
+  p.q = static_cast<const uint16_t*>(q);
+  p.o = static_cast<uint16_t*>(o);
+  p.lse = lse;
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_rl = reinterpret_cast<float2*>(ws + w.rl);
+  p.split = reinterpret_cast<int4*>(ws + w.split);
+  p.Hq = Hq;
+  p.group = Hq / Hkv;
+  p.causal = causal;
+  p.min_units = 16;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.timeout_ns = wait_budget_ns();
+  // no more CTAs than the longest possible caches have ranges
+  const long long most = ((long long)total_q * p.group / (8 * nt) + num_seqs) * Hkv *
+                         std::max(1LL, ((long long)max_pages * page_size + kKv4Tile - 1) / kKv4Tile);
+  const int ctas = (int)std::max(1LL, std::min<long long>(max_ctas(d, nt), most / p.min_units));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  switch (d) {
+    case 64: e = nt == 1 ? launch_kv4<64, 1>(p, ctas, st) : launch_kv4<64, 2>(p, ctas, st); break;
+    case 96: e = nt == 1 ? launch_kv4<96, 1>(p, ctas, st) : launch_kv4<96, 2>(p, ctas, st); break;
+    case 128: e = nt == 1 ? launch_kv4<128, 1>(p, ctas, st) : launch_kv4<128, 2>(p, ctas, st); break;
+    default: e = launch_kv4<256, 1>(p, ctas, st); break;
+  }
+  return cuda_error_status(e);
+}
+
+}  // extern "C"

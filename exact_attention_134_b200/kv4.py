@@ -1,0 +1,187 @@
+"""The paged 4-bit key/value cache and attention over it.
+
+    pool = kv4_alloc(num_pages, Hkv, d, page_size)               # uint8, one layer
+    kv4_append(k, v, pool, page_table, seq_lens)                 # new tokens in
+    o, lse = attn_fwd_kv4(q, pool, page_table, seq_lens, causal=True)        # decoding
+    k, v = kv4_gather(pool, page_table, seq_lens, total, cu)     # a prompt's chunk: bf16 for attn_fwd_varlen
+
+Keys and values are held in pages of page_size tokens, 5 bits a value: a bf16
+minimum and scale and 4-bit codes for every token, kv head and 32 channels
+(include/attn.h has the definition, csrc/kv4_format.cuh the layout). page_table
+(int32 [num_seqs, max_pages]) says in which page token j of sequence s is:
+page_table[s, j // page_size]. seq_lens (int32 [num_seqs]) counts the tokens in
+the cache, those of the call included: a call's rows are its sequences' last
+tokens. kv4_pages.KV4Pages keeps the table on the host.
+
+A page id outside the pool is not followed: get_status() then reports
+ATTN_ERR_INVALID_ARG with where = 0x500 (attention), 0x510 (append), 0x520
+(gather) or 0x530 (copy).
+"""
+from __future__ import annotations
+
+import math
+
+from . import _check, _current_device, _stream_handle, lib
+
+
+def kv4_page_bytes(Hkv: int, d: int, page_size: int) -> int:
+    """Bytes of a page in one layer; 0 for sizes that the cache does not have."""
+    return int(lib().attn_kv4_page_bytes(int(Hkv), int(d), int(page_size)))
+
+
+def kv4_alloc(num_pages: int, Hkv: int, d: int, page_size: int, num_layers: int | None = None, device="cuda"):
+    """A pool of pages: uint8 [num_pages, Hkv, page_size // 16, 20 d], with
+    num_layers a leading axis of layers (pool[i] is layer i's pool). Its contents
+    need no initial value."""
+    import torch
+    if kv4_page_bytes(Hkv, d, page_size) == 0:
+        raise ValueError("page_size must be a power of two from 16 to 1024 and d 64, 96, 128 or 256")
+    shape = (num_pages, Hkv, page_size // 16, 20 * d)
+    return torch.empty(shape if num_layers is None else (num_layers, *shape), dtype=torch.uint8, device=device)
+
+
+def _cache_args(pool, page_table, seq_lens, cu_seqlens, d=None):
+    """(num_seqs, max_pages, num_pages, page_size, Hkv, d) after the checks that all calls share."""
+    import torch
+    if pool.dtype != torch.uint8 or not pool.is_cuda or not pool.is_contiguous() or pool.dim() != 4 or \
+            pool.shape[3] % 20:
+        raise ValueError("pool must be a contiguous uint8 CUDA tensor [num_pages, Hkv, page_size / 16, 20 d]")
+    for name, t, dim in (("page_table", page_table, 2), ("seq_lens", seq_lens, 1), ("cu_seqlens", cu_seqlens, 1)):
+        if t is None and name == "cu_seqlens":
+            continue
+        if t.dtype != torch.int32 or t.device != pool.device or not t.is_contiguous() or t.dim() != dim:
+            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {dim} dimension(s) on the pool's device")
+    num_pages, Hkv, tiles, record = pool.shape
+    if seq_lens.numel() != page_table.shape[0]:
+        raise ValueError("page_table and seq_lens must hold the same sequences")
+    if cu_seqlens is not None and cu_seqlens.numel() != seq_lens.numel() + 1:
+        raise ValueError("cu_seqlens must hold num_seqs + 1 offsets")
+    if d is not None and record != 20 * d:
+        raise ValueError(f"the pool holds records of d = {record // 20}, not {d}")
+    return page_table.shape[0], page_table.shape[1], num_pages, 16 * tiles, Hkv, record // 20
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def kv4_append(k, v, pool, page_table, seq_lens, cu_seqlens=None):
+    """Writes new tokens into the cache.
+
+    k, v: bf16 cuda [total, Hkv, d], any strides that are multiples of 8 elements,
+    channels contiguous. Sequence s's rows are cu_seqlens[s] .. cu_seqlens[s + 1]
+    - 1 (int32 cuda [num_seqs + 1]; None: total / num_seqs each), its last tokens
+    of seq_lens[s]. A page shared by several sequences is copied before one of
+    them appends to it (KV4Pages.extend names the copies)."""
+    import torch
+    for name, t in (("k", k), ("v", v)):
+        if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+            raise ValueError(f"{name} must be a bf16 CUDA tensor [total, Hkv, d] with contiguous channels")
+        if t.device != pool.device:
+            raise ValueError(f"{name} must be on the pool's device")
+    total, Hkv, d = k.shape
+    n, max_pages, num_pages, page_size, pool_heads, _ = _cache_args(pool, page_table, seq_lens, cu_seqlens, d)
+    if tuple(v.shape) != tuple(k.shape) or Hkv != pool_heads:
+        raise ValueError(f"shape mismatch: k {tuple(k.shape)} v {tuple(v.shape)} pool {tuple(pool.shape)}")
+    # the stride of an axis of one is never used: torch leaves anything there
+    strides = [t.stride(i) if t.shape[i] > 1 else 0 for t in (k, v) for i in (0, 1)]
+    with _current_device(pool.device):
+        st = lib().attn_kv4_append(k.data_ptr(), v.data_ptr(), *strides, pool.data_ptr(), page_table.data_ptr(),
+                                   seq_lens.data_ptr(), _ptr(cu_seqlens), n, max_pages, num_pages, page_size, total,
+                                   Hkv, d, _stream_handle(pool.device))
+    _check(st, "attn_kv4_append")
+
+
+def kv4_gather(pool, page_table, seq_lens, total: int, cu_seqlens=None, k=None, v=None):
+    """Reads tokens back as bf16 [total, Hkv, d] each: the last cu_seqlens[s + 1] -
+    cu_seqlens[s] tokens of every sequence (None: total / num_seqs), packed as
+    attn_fwd_varlen takes them. Rows that no sequence owns are left as they were.
+    Returns (k, v)."""
+    import torch
+    n, max_pages, num_pages, page_size, Hkv, d = _cache_args(pool, page_table, seq_lens, cu_seqlens)
+    total = int(total)
+    k = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=pool.device) if k is None else k
+    v = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=pool.device) if v is None else v
+    for name, t in (("k", k), ("v", v)):
+        if t.dtype != torch.bfloat16 or t.device != pool.device or not t.is_contiguous() or \
+                tuple(t.shape) != (total, Hkv, d):
+            raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor {(total, Hkv, d)} on the pool's device")
+    with _current_device(pool.device):
+        st = lib().attn_kv4_gather(pool.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_seqlens), n,
+                                   max_pages, num_pages, page_size, total, Hkv, d, k.data_ptr(), v.data_ptr(),
+                                   _stream_handle(pool.device))
+    _check(st, "attn_kv4_gather")
+    return k, v
+
+
+def kv4_copy_pages(pool, src, dst):
+    """Copies pages within the pool, in every layer: page dst[i] = page src[i].
+
+    pool: [num_pages, ...] of one layer (4-D) or [num_layers, num_pages, ...]
+    (5-D). src, dst: int32 cuda vectors; no dst may be another pair's dst or src."""
+    import torch
+    if pool.dtype != torch.uint8 or not pool.is_cuda or not pool.is_contiguous() or pool.dim() not in (4, 5):
+        raise ValueError("pool must be a contiguous uint8 CUDA tensor of 4 dimensions, or 5 with layers")
+    for name, t in (("src", src), ("dst", dst)):
+        if t.dtype != torch.int32 or t.device != pool.device or not t.is_contiguous() or t.dim() != 1:
+            raise ValueError(f"{name} must be a contiguous int32 CUDA vector on the pool's device")
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst must have the same length")
+    layers, num_pages = (1, pool.shape[0]) if pool.dim() == 4 else pool.shape[:2]
+    page_bytes = pool[0].numel() if pool.dim() == 4 else pool[0, 0].numel()
+    with _current_device(pool.device):
+        st = lib().attn_kv4_copy_pages(pool.data_ptr(), layers, num_pages, page_bytes, src.data_ptr(), dst.data_ptr(),
+                                       src.numel(), _stream_handle(pool.device))
+    _check(st, "attn_kv4_copy_pages")
+
+
+def fwd_kv4_workspace_size(Hq: int, Hkv: int, max_seqlen_q: int, d: int) -> int:
+    """Bytes of scratch that attn_fwd_kv4 needs (some 6 MB at most; any number of sequences)."""
+    return int(lib().attn_fwd_kv4_workspace_size(Hq, Hkv, int(max_seqlen_q), d))
+
+
+def attn_fwd_kv4(q, pool, page_table, seq_lens, cu_seqlens_q=None, max_seqlen_q: int | None = None,
+                 causal: bool = False, scale: float | None = None, workspace=None, out=None, lse=None):
+    """Attention of a few query tokens a sequence over the 4-bit cache (decoding;
+    drafted tokens checked together).
+
+    q: bf16 cuda [total_q, Hq, d], sequence s's rows cu_seqlens_q[s] ..
+    cu_seqlens_q[s + 1] - 1 (None: total_q / num_seqs each), standing at its last
+    tokens: with causal, row i of n sees tokens 0 .. seq_lens[s] - n + i.
+    max_seqlen_q: the longest sequence's query rows (a bound of them chooses the
+    kernel; total_q / num_seqs, rounded up, when not given). workspace: a uint8
+    cuda buffer of fwd_kv4_workspace_size(Hq, Hkv, max_seqlen_q, d) bytes, one
+    for each call that may run at the same time (allocated here if None).
+    Returns (o bf16 [total_q, Hq, d], lse fp32 [Hq, total_q]); a row that sees no
+    token gets o = 0 and lse = -inf.
+    """
+    import torch
+    if q.dtype != torch.bfloat16 or not q.is_cuda or not q.is_contiguous() or q.dim() != 3:
+        raise ValueError("q must be a contiguous bf16 CUDA tensor [total, H, d]")
+    if q.device != pool.device:
+        raise ValueError("q must be on the pool's device")
+    total, Hq, d = q.shape
+    n, max_pages, num_pages, page_size, Hkv, _ = _cache_args(pool, page_table, seq_lens, cu_seqlens_q, d)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if max_seqlen_q is None:
+        max_seqlen_q = -(-total // max(n, 1))
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
+    for name, t, dtype, shape in (("out", out, torch.bfloat16, (total, Hq, d)), ("lse", lse, torch.float32, (Hq, total))):
+        if t.dtype != dtype or t.device != q.device or not t.is_contiguous() or tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {shape} on the device of q")
+    if workspace is None:
+        workspace = torch.empty(fwd_kv4_workspace_size(Hq, Hkv, max_seqlen_q, d), dtype=torch.uint8, device=q.device)
+    elif workspace.device != q.device:
+        raise ValueError("workspace must be on the device of q")
+    with _current_device(q.device):
+        st = lib().attn_fwd_kv4(q.data_ptr(), pool.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
+                                _ptr(cu_seqlens_q), out.data_ptr(), lse.data_ptr(), n, max_pages, num_pages, page_size,
+                                int(max_seqlen_q), total, Hq, Hkv, d, int(bool(causal)), float(scale),
+                                workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                _stream_handle(q.device))
+    _check(st, "attn_fwd_kv4")
+    return out, lse

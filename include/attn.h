@@ -1,6 +1,8 @@
 /*
  * attn.h — C ABI of the B200 (sm_100a) fused exact attention: forward (bf16,
- * 8-bit, packed sequences, key-range partials and their merge) and backward.
+ * 8-bit, packed sequences, key-range partials and their merge) and backward;
+ * the norm and rotation of queries and keys before it; the paged 4-bit
+ * key/value cache and attention over it.
  *
  * Operation (the definition on "FlashAttention (TR)", systems-analysis.info,
  * section "Standart Attention Mekanizmasının Sorunları"):
@@ -382,9 +384,176 @@ ATTN_API attn_status_t attn_bwd_varlen(const void* q, const void* k, const void*
                                        size_t workspace_bytes, void* stream);
 
 /*
+ * attn_qk_norm_rope — queries and keys between their projection and attention:
+ * the RMS norm of every head, then the rotation by the position, in one pass.
+ *     xhat = x / sqrt(mean(x^2) + eps),   n = xhat * w
+ *     pair i = (a, b) of n:  a' = a cos t - b sin t,  b' = a sin t + b cos t,
+ *     t = position[axis of i] * inv_freq[i]
+ * computed in fp32 (the angle in fp64, reduced to a fraction of a turn) and
+ * rounded once.
+ *   q, k           device, bf16, rows of d values at
+ *                  b * strides[0] + h * strides[1] + n * strides[2] (read)
+ *   q_out, k_out   device, bf16, the same with their own strides (written);
+ *                  each may be q or k itself with the same strides, and
+ *                  overlaps no other tensor of the call otherwise
+ *   strides        host, 3 (batch, head, token) each for q, k, q_out, k_out, in
+ *                  elements, >= 0 and multiples of 8
+ *   q_weight, k_weight  device [d], fp32, or bf16 with weight_bf16 = 1; both
+ *                  NULL: no norm, rotation only (eps is then not looked at)
+ *   positions      device, int32: axis a, batch b, token n at
+ *                  a * pos_axis_stride + b * pos_batch_stride + n (a batch
+ *                  stride of 0: the same positions for all)
+ *   inv_freq       device, fp32 [rotary_dim / 2]
+ *   sections       host, num_axes counts (1 to 4 axes) that add up to
+ *                  rotary_dim / 2: the first sections[0] pairs turn with axis 0
+ *                  (time, say), the next sections[1] with axis 1, and so on
+ *   rotary_dim     0 .. d, a multiple of 16; the other channels are normed and
+ *                  not rotated; 0: positions, inv_freq and sections are unused
+ *   interleaved    0: pair i is channels (i, i + rotary_dim / 2); 1: (2i, 2i + 1)
+ *   d              64, 96, 128 or 256
+ * Packed sequences are B = 1 with N = total rows. One launch; allocates nothing.
+ */
+ATTN_API attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
+                                         const long long* strides, const void* q_weight,
+                                         const void* k_weight, int weight_bf16,
+                                         const int* positions, long long pos_axis_stride,
+                                         long long pos_batch_stride, const float* inv_freq,
+                                         const int* sections, int num_axes, int rotary_dim,
+                                         int interleaved, int B, int N, int Hq, int Hkv, int d,
+                                         float eps, void* stream);
+
+/*
+ * attn_qk_norm_rope_bwd — its gradients: with dn the rotation of the result's
+ * gradient by -t and g = dn * w,
+ *     dx = (g - xhat * mean(g * xhat)) / sqrt(mean(x^2) + eps),
+ *     dw = sum over batch, heads and tokens of dn * xhat.
+ *   q, k             the forward's inputs (not read without a norm)
+ *   dq_out, dk_out   device, bf16, gradients of q_out, k_out (read)
+ *   dq, dk           device, bf16, gradients of q, k (written; each may be
+ *                    dq_out or dk_out itself with the same strides)
+ *   strides          host, 3 each for q, k, dq_out, dk_out, dq, dk
+ *   dq_weight, dk_weight  device, fp32 [d] (written; unused without a norm)
+ *   workspace        device, attn_qk_norm_rope_bwd_workspace_size() bytes,
+ *                    16-byte aligned, with a norm only: partial weight
+ *                    gradients; needs no initial value
+ * The other arguments are the forward's. Deterministic: sums are taken in a
+ * fixed order. Two launches with a norm, one without.
+ */
+ATTN_API size_t attn_qk_norm_rope_bwd_workspace_size(int B, int N, int Hq, int Hkv, int d);
+ATTN_API attn_status_t attn_qk_norm_rope_bwd(
+    const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq, void* dk,
+    const long long* strides, const void* q_weight, const void* k_weight, int weight_bf16,
+    float* dq_weight, float* dk_weight, const int* positions, long long pos_axis_stride,
+    long long pos_batch_stride, const float* inv_freq, const int* sections, int num_axes,
+    int rotary_dim, int interleaved, int B, int N, int Hq, int Hkv, int d, float eps,
+    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The 4-bit key/value cache. Keys and values are held in pages of page_size
+ * tokens, 5 bits a value: for every token, kv head and group of 32 channels a
+ * bf16 minimum lo and scale s and 4-bit codes, standing for lo + s * code with
+ *     lo = min_c x_c,  s = bf16((max_c x_c - lo) / 15),
+ *     code_c = min(rne((x_c - lo) / s), 15).
+ * A group with a spread below 15 * 2^-126 is held as its minimum; a group with
+ * a NaN or an infinity is held as NaN.
+ *   pool        device, uint8 [num_pages][Hkv][page_size / 16][20 d],
+ *               16-byte aligned; one page is attn_kv4_page_bytes() bytes. The
+ *               record of 16 tokens is laid out in csrc/kv4_format.cuh. Needs
+ *               no initial value: what was not appended is never used
+ *   page_size   16, 32, ... 1024 (a power of two); d = 64, 96, 128 or 256
+ *   page_table  device, int32 [num_seqs][max_pages]: token j of sequence s is
+ *               in page page_table[s][j / page_size]; entries behind a
+ *               sequence's last token are not read. A page may belong to
+ *               several sequences (a shared prefix)
+ *   seq_lens    device, int32 [num_seqs]: tokens in the cache, those of the
+ *               call included (values outside [0, max_pages * page_size] are
+ *               clamped)
+ *   cu_seqlens  device, int32 [num_seqs + 1]: the call's rows of sequence s are
+ *               cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (non-decreasing; rows
+ *               outside [0, total] are clamped away), or NULL: total / num_seqs
+ *               rows each. The n rows of a sequence are its LAST n tokens: row
+ *               i is token seq_lens[s] - n + i
+ * A page id outside [0, num_pages) where one is needed is not followed: the
+ * kernel records ATTN_ERR_INVALID_ARG (where = 0x5..) in the device status
+ * word and goes on without those tokens.
+ */
+ATTN_API size_t attn_kv4_page_bytes(int Hkv, int d, int page_size);
+
+/*
+ * attn_kv4_append — writes new tokens into the cache.
+ *   k, v    device, bf16, row t, head h at t * token_stride + h * head_stride
+ *           (elements; >= 0, multiples of 8)
+ * Rows at a token below 0 (n > seq_lens) are left out. No two rows of a call
+ * may be the same token of the same page: a page that several sequences share
+ * is copied before one of them appends to it. One launch; allocates nothing.
+ */
+ATTN_API attn_status_t attn_kv4_append(const void* k, const void* v, long long k_token_stride,
+                                       long long k_head_stride, long long v_token_stride,
+                                       long long v_head_stride, void* pool, const int* page_table,
+                                       const int* seq_lens, const int* cu_seqlens, int num_seqs,
+                                       int max_pages, int num_pages, int page_size, int total,
+                                       int Hkv, int d, void* stream);
+
+/*
+ * attn_kv4_gather — reads tokens back as bf16, packed as attn_fwd_varlen takes
+ * them: k, v [total, Hkv, d] (written; rows that no sequence owns are left as
+ * they were, rows at a token below 0 or on a bad page are 0). With
+ * cu_seqlens = the offsets of seq_lens this is the whole context, for the
+ * attention of a chunk of many query tokens. One launch; allocates nothing.
+ */
+ATTN_API attn_status_t attn_kv4_gather(const void* pool, const int* page_table,
+                                       const int* seq_lens, const int* cu_seqlens, int num_seqs,
+                                       int max_pages, int num_pages, int page_size, int total,
+                                       int Hkv, int d, void* k, void* v, void* stream);
+
+/*
+ * attn_kv4_copy_pages — copies whole pages within the pool, in every layer:
+ * page dst[i] = page src[i] for all i.
+ *   pool        device, [num_layers][num_pages][page_bytes], 16-byte aligned
+ *   page_bytes  a multiple of 16 (attn_kv4_page_bytes(), or any other cache's)
+ *   src, dst    device, int32 [num_pairs]. The pairs are copied in no order: no
+ *               dst may be another pair's dst or src (src = dst is a no-op).
+ *               Ids outside [0, num_pages) are left out and recorded like bad
+ *               pages above
+ * One launch; allocates nothing.
+ */
+ATTN_API attn_status_t attn_kv4_copy_pages(void* pool, int num_layers, int num_pages,
+                                           size_t page_bytes, const int* src, const int* dst,
+                                           int num_pairs, void* stream);
+
+/*
+ * attn_fwd_kv4 — attention of a few query tokens a sequence over the 4-bit
+ * cache (decoding; drafted tokens checked together): O and LSE as attn_fwd,
+ * over what the cache stands for, exactly (keys and values are not rounded
+ * again).
+ *   q, o     device, bf16 [total_q, Hq, d]    (o written)
+ *   lse      device, fp32 [Hq, total_q]       (written)
+ *   pool, page_table, seq_lens, cu_seqlens_q  as above: the query rows of a
+ *            sequence stand at its last tokens; with causal = 1 row i of n sees
+ *            tokens 0 .. seq_lens - n + i, with causal = 0 all of them. A row
+ *            that sees none gets O = 0 and LSE = -inf
+ *   max_seqlen_q  bounds every sequence's query rows: it chooses between 8 and
+ *            16 rows a pass (a larger sequence is computed all the same)
+ *   workspace  device scratch of attn_fwd_kv4_workspace_size() bytes, 16-byte
+ *            aligned, for one call at a time; needs no initial value
+ * Any number of query rows is computed, 8 or 16 (row, head) pairs of a kv head
+ * in one pass over its cache; for long chunks attn_kv4_gather and
+ * attn_fwd_varlen are faster. |v| up to 2^64. Two launches (attention, merge of
+ * what was split); allocates nothing; deterministic.
+ */
+ATTN_API size_t attn_fwd_kv4_workspace_size(int Hq, int Hkv, int max_seqlen_q, int d);
+ATTN_API attn_status_t attn_fwd_kv4(const void* q, const void* pool, const int* page_table,
+                                    const int* seq_lens, const int* cu_seqlens_q, void* o,
+                                    float* lse, int num_seqs, int max_pages, int num_pages,
+                                    int page_size, int max_seqlen_q, int total_q, int Hq, int Hkv,
+                                    int d, int causal, float scale, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
  * attn_get_status — synchronises `stream`, returns and clears the device
- * status word (ATTN_OK, or ATTN_ERR_TIMEOUT if a kernel gave up on a pipeline
- * wait since the last call). Returns ATTN_ERR_CUDA if synchronisation fails.
+ * status word (ATTN_OK, ATTN_ERR_TIMEOUT if a kernel gave up on a pipeline
+ * wait since the last call, or ATTN_ERR_INVALID_ARG if one met a page id
+ * outside the 4-bit cache's pool). Returns ATTN_ERR_CUDA if synchronisation fails.
  */
 ATTN_API attn_status_t attn_get_status(void* stream);
 

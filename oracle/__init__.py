@@ -15,6 +15,8 @@ Modules
   backward   gradients dQ, dK, dV of the definition, in fp64
   partial    attention over a range of keys (global causal mask) and the
              exact merge of partial results by their LSE
+  norm_rope  RMS norm of heads, rotation by position, and their gradients
+  kv4        the 4-bit cache: quantisation, records, attention over them
 
 Pins (tests/test_oracle.py, CPU-only) tie every function to something other
 than itself: brute force on tiny inputs, closed forms, invariants the pages
@@ -31,3 +33,4 @@ from .attention import (attention_fp64, attention_f64, attention_varlen_fp64,  #
 from . import quant8  # noqa: F401
 from .backward import attention_bwd_fp64  # noqa: F401
 from .partial import attention_partial_fp64, merge_partials_fp64  # noqa: F401
+from . import kv4, norm_rope  # noqa: F401
