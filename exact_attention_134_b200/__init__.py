@@ -119,26 +119,24 @@ def _check(status: int, what: str):
 
 def _stream_handle(device=None) -> int:
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    if device is None or device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    # the handle alone: a Stream object costs 2 us, as long as a launch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-class _current_device:
-    """Makes `device` the current one for a call (the library launches there)."""
-
-    def __init__(self, device):
-        self.device = device
-
-    def __enter__(self):
-        import torch
-        here = torch.cuda.current_device()
-        self.back = None if here == self.device.index else here
-        if self.back is not None:
-            torch.cuda.set_device(self.device)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            import torch
-            torch.cuda.set_device(self.back)
+def _call(name, index, *args):
+    """Calls an entry point with device `index` current (the library launches
+    there), the device's current stream as its last argument, and checks its status."""
+    import torch
+    fn = getattr(_lib or lib(), name)
+    here = torch.cuda.current_device()
+    if here == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    _check(status, name)
 
 
 def _shape_args(q, k, v):

@@ -21,7 +21,7 @@ from __future__ import annotations
 
 import math
 
-from . import _check, _current_device, _stream_handle, lib
+from . import _call, lib
 
 
 def kv4_page_bytes(Hkv: int, d: int, page_size: int) -> int:
@@ -41,24 +41,26 @@ def kv4_alloc(num_pages: int, Hkv: int, d: int, page_size: int, num_layers: int 
 
 
 def _cache_args(pool, page_table, seq_lens, cu_seqlens, d=None):
-    """(num_seqs, max_pages, num_pages, page_size, Hkv, d) after the checks that all calls share."""
+    """(num_seqs, max_pages, num_pages, page_size, Hkv, d, device index) after the checks that all calls share."""
     import torch
-    if pool.dtype != torch.uint8 or not pool.is_cuda or not pool.is_contiguous() or pool.dim() != 4 or \
-            pool.shape[3] % 20:
+    index = pool.get_device()
+    shape = pool.shape
+    if pool.dtype is not torch.uint8 or index < 0 or len(shape) != 4 or shape[3] % 20 or not pool.is_contiguous():
         raise ValueError("pool must be a contiguous uint8 CUDA tensor [num_pages, Hkv, page_size / 16, 20 d]")
     for name, t, dim in (("page_table", page_table, 2), ("seq_lens", seq_lens, 1), ("cu_seqlens", cu_seqlens, 1)):
-        if t is None and name == "cu_seqlens":
+        if t is None and dim == 1 and name == "cu_seqlens":
             continue
-        if t.dtype != torch.int32 or t.device != pool.device or not t.is_contiguous() or t.dim() != dim:
+        if t.dtype is not torch.int32 or t.get_device() != index or t.dim() != dim or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {dim} dimension(s) on the pool's device")
-    num_pages, Hkv, tiles, record = pool.shape
-    if seq_lens.numel() != page_table.shape[0]:
+    num_pages, Hkv, tiles, record = shape
+    n, max_pages = page_table.shape
+    if seq_lens.shape[0] != n:
         raise ValueError("page_table and seq_lens must hold the same sequences")
-    if cu_seqlens is not None and cu_seqlens.numel() != seq_lens.numel() + 1:
+    if cu_seqlens is not None and cu_seqlens.shape[0] != n + 1:
         raise ValueError("cu_seqlens must hold num_seqs + 1 offsets")
     if d is not None and record != 20 * d:
         raise ValueError(f"the pool holds records of d = {record // 20}, not {d}")
-    return page_table.shape[0], page_table.shape[1], num_pages, 16 * tiles, Hkv, record // 20
+    return n, max_pages, num_pages, 16 * tiles, Hkv, record // 20, index
 
 
 def _ptr(t):
@@ -74,22 +76,22 @@ def kv4_append(k, v, pool, page_table, seq_lens, cu_seqlens=None):
     of seq_lens[s]. A page shared by several sequences is copied before one of
     them appends to it (KV4Pages.extend names the copies)."""
     import torch
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape:
+        raise ValueError(f"k and v must both be [total, Hkv, d], not {tuple(shape)} and {tuple(v.shape)}")
+    total, Hkv, d = shape
+    n, max_pages, num_pages, page_size, pool_heads, _, index = _cache_args(pool, page_table, seq_lens, cu_seqlens, d)
+    if Hkv != pool_heads:
+        raise ValueError(f"the pool holds {pool_heads} kv heads, not {Hkv}")
+    strides = []
     for name, t in (("k", k), ("v", v)):
-        if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-            raise ValueError(f"{name} must be a bf16 CUDA tensor [total, Hkv, d] with contiguous channels")
-        if t.device != pool.device:
-            raise ValueError(f"{name} must be on the pool's device")
-    total, Hkv, d = k.shape
-    n, max_pages, num_pages, page_size, pool_heads, _ = _cache_args(pool, page_table, seq_lens, cu_seqlens, d)
-    if tuple(v.shape) != tuple(k.shape) or Hkv != pool_heads:
-        raise ValueError(f"shape mismatch: k {tuple(k.shape)} v {tuple(v.shape)} pool {tuple(pool.shape)}")
-    # the stride of an axis of one is never used: torch leaves anything there
-    strides = [t.stride(i) if t.shape[i] > 1 else 0 for t in (k, v) for i in (0, 1)]
-    with _current_device(pool.device):
-        st = lib().attn_kv4_append(k.data_ptr(), v.data_ptr(), *strides, pool.data_ptr(), page_table.data_ptr(),
-                                   seq_lens.data_ptr(), _ptr(cu_seqlens), n, max_pages, num_pages, page_size, total,
-                                   Hkv, d, _stream_handle(pool.device))
-    _check(st, "attn_kv4_append")
+        s = t.stride()
+        if t.dtype is not torch.bfloat16 or t.get_device() != index or (s[2] != 1 and d > 1):
+            raise ValueError(f"{name} must be a bf16 CUDA tensor with contiguous channels on the pool's device")
+        # the stride of an axis of one is never used: torch leaves anything there
+        strides += (s[0] if total > 1 else 0, s[1] if Hkv > 1 else 0)
+    _call("attn_kv4_append", index, k.data_ptr(), v.data_ptr(), *strides, pool.data_ptr(), page_table.data_ptr(),
+          seq_lens.data_ptr(), _ptr(cu_seqlens), n, max_pages, num_pages, page_size, total, Hkv, d)
 
 
 def kv4_gather(pool, page_table, seq_lens, total: int, cu_seqlens=None, k=None, v=None):
@@ -98,19 +100,16 @@ def kv4_gather(pool, page_table, seq_lens, total: int, cu_seqlens=None, k=None, 
     attn_fwd_varlen takes them. Rows that no sequence owns are left as they were.
     Returns (k, v)."""
     import torch
-    n, max_pages, num_pages, page_size, Hkv, d = _cache_args(pool, page_table, seq_lens, cu_seqlens)
-    total = int(total)
-    k = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=pool.device) if k is None else k
-    v = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=pool.device) if v is None else v
+    n, max_pages, num_pages, page_size, Hkv, d, index = _cache_args(pool, page_table, seq_lens, cu_seqlens)
+    shape = (int(total), Hkv, d)
     for name, t in (("k", k), ("v", v)):
-        if t.dtype != torch.bfloat16 or t.device != pool.device or not t.is_contiguous() or \
-                tuple(t.shape) != (total, Hkv, d):
-            raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor {(total, Hkv, d)} on the pool's device")
-    with _current_device(pool.device):
-        st = lib().attn_kv4_gather(pool.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_seqlens), n,
-                                   max_pages, num_pages, page_size, total, Hkv, d, k.data_ptr(), v.data_ptr(),
-                                   _stream_handle(pool.device))
-    _check(st, "attn_kv4_gather")
+        if t is not None and (t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape or
+                              not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor {shape} on the pool's device")
+    k = torch.empty(shape, dtype=torch.bfloat16, device=pool.device) if k is None else k
+    v = torch.empty_like(k) if v is None else v
+    _call("attn_kv4_gather", index, pool.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_seqlens), n,
+          max_pages, num_pages, page_size, shape[0], Hkv, d, k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -120,19 +119,18 @@ def kv4_copy_pages(pool, src, dst):
     pool: [num_pages, ...] of one layer (4-D) or [num_layers, num_pages, ...]
     (5-D). src, dst: int32 cuda vectors; no dst may be another pair's dst or src."""
     import torch
-    if pool.dtype != torch.uint8 or not pool.is_cuda or not pool.is_contiguous() or pool.dim() not in (4, 5):
+    index, shape = pool.get_device(), pool.shape
+    if pool.dtype is not torch.uint8 or index < 0 or len(shape) not in (4, 5) or not pool.is_contiguous():
         raise ValueError("pool must be a contiguous uint8 CUDA tensor of 4 dimensions, or 5 with layers")
     for name, t in (("src", src), ("dst", dst)):
-        if t.dtype != torch.int32 or t.device != pool.device or not t.is_contiguous() or t.dim() != 1:
+        if t.dtype is not torch.int32 or t.get_device() != index or t.dim() != 1 or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 CUDA vector on the pool's device")
-    if src.numel() != dst.numel():
+    n = src.shape[0]
+    if dst.shape[0] != n:
         raise ValueError("src and dst must have the same length")
-    layers, num_pages = (1, pool.shape[0]) if pool.dim() == 4 else pool.shape[:2]
-    page_bytes = pool[0].numel() if pool.dim() == 4 else pool[0, 0].numel()
-    with _current_device(pool.device):
-        st = lib().attn_kv4_copy_pages(pool.data_ptr(), layers, num_pages, page_bytes, src.data_ptr(), dst.data_ptr(),
-                                       src.numel(), _stream_handle(pool.device))
-    _check(st, "attn_kv4_copy_pages")
+    layers, num_pages, H, tiles, record = shape if len(shape) == 5 else (1, *shape)
+    _call("attn_kv4_copy_pages", index, pool.data_ptr(), layers, num_pages, H * tiles * record, src.data_ptr(),
+          dst.data_ptr(), n)
 
 
 def fwd_kv4_workspace_size(Hq: int, Hkv: int, max_seqlen_q: int, d: int) -> int:
@@ -156,32 +154,30 @@ def attn_fwd_kv4(q, pool, page_table, seq_lens, cu_seqlens_q=None, max_seqlen_q:
     token gets o = 0 and lse = -inf.
     """
     import torch
-    if q.dtype != torch.bfloat16 or not q.is_cuda or not q.is_contiguous() or q.dim() != 3:
-        raise ValueError("q must be a contiguous bf16 CUDA tensor [total, H, d]")
-    if q.device != pool.device:
-        raise ValueError("q must be on the pool's device")
-    total, Hq, d = q.shape
-    n, max_pages, num_pages, page_size, Hkv, _ = _cache_args(pool, page_table, seq_lens, cu_seqlens_q, d)
+    shape = q.shape
+    if q.dtype is not torch.bfloat16 or len(shape) != 3 or q.get_device() != pool.get_device() or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 CUDA tensor [total, H, d] on the pool's device")
+    total, Hq, d = shape
+    n, max_pages, num_pages, page_size, Hkv, _, index = _cache_args(pool, page_table, seq_lens, cu_seqlens_q, d)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if max_seqlen_q is None:
         max_seqlen_q = -(-total // max(n, 1))
     if out is None:
         out = torch.empty_like(q)
+    elif out.dtype is not torch.bfloat16 or out.get_device() != index or out.shape != shape or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous bf16 CUDA tensor {tuple(shape)} on the device of q")
     if lse is None:
         lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
-    for name, t, dtype, shape in (("out", out, torch.bfloat16, (total, Hq, d)), ("lse", lse, torch.float32, (Hq, total))):
-        if t.dtype != dtype or t.device != q.device or not t.is_contiguous() or tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {shape} on the device of q")
+    elif lse.dtype is not torch.float32 or lse.get_device() != index or lse.shape != (Hq, total) or \
+            not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous fp32 CUDA tensor {(Hq, total)} on the device of q")
     if workspace is None:
         workspace = torch.empty(fwd_kv4_workspace_size(Hq, Hkv, max_seqlen_q, d), dtype=torch.uint8, device=q.device)
-    elif workspace.device != q.device:
+    elif workspace.get_device() != index:
         raise ValueError("workspace must be on the device of q")
-    with _current_device(q.device):
-        st = lib().attn_fwd_kv4(q.data_ptr(), pool.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
-                                _ptr(cu_seqlens_q), out.data_ptr(), lse.data_ptr(), n, max_pages, num_pages, page_size,
-                                int(max_seqlen_q), total, Hq, Hkv, d, int(bool(causal)), float(scale),
-                                workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                _stream_handle(q.device))
-    _check(st, "attn_fwd_kv4")
+    _call("attn_fwd_kv4", index, q.data_ptr(), pool.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
+          _ptr(cu_seqlens_q), out.data_ptr(), lse.data_ptr(), n, max_pages, num_pages, page_size, int(max_seqlen_q),
+          total, Hq, Hkv, d, 1 if causal else 0, float(scale), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     return out, lse

@@ -12,100 +12,108 @@ and attn_fwd_kv4 (3-D) read them.
 """
 from __future__ import annotations
 
-from . import _check, _current_device, _ll, _c_int, _stream_handle, lib
+import struct
+
+from . import _c_int, _call, lib
+
+_pack12, _pack18 = struct.Struct("12q").pack, struct.Struct("18q").pack
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _rows(name, t, shape=None):
-    """(batch, head, token) strides of a [B, H, N, d] or [total, H, d] tensor."""
-    import torch
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() not in (3, 4):
-        raise ValueError(f"{name} must be a bf16 CUDA tensor [B, H, N, d] or [total, H, d]")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
-    s = t.stride()
-    if s[-1] != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name} must have contiguous channels")
-    s = (0, s[1], s[0]) if t.dim() == 3 else s[:3]
-    # the stride of an axis of one is never used: torch leaves anything there
-    n = (1, t.shape[1], t.shape[0]) if t.dim() == 3 else t.shape[:3]
-    return [x if m > 1 else 0 for x, m in zip(s, n)]
-
-
-def _written(name, t):
-    if any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)):
-        raise ValueError(f"{name} is written to and must not be expanded")
-
-
 def _shapes(q, k):
-    if q.dim() != k.dim() or q.shape[-1] != k.shape[-1]:
-        raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)}")
-    if q.dim() == 3:
-        (N, Hq, d), B, Hkv = q.shape, 1, k.shape[1]
-        same = k.shape[0] == N
+    """(B, N, Hq, Hkv, d) of q and k."""
+    sq, sk = q.shape, k.shape
+    if len(sq) == 4 and len(sk) == 4:
+        B, Hq, N, d = sq
+        Bk, Hkv, Nk, dk = sk
+    elif len(sq) == 3 and len(sk) == 3:
+        (N, Hq, d), (Nk, Hkv, dk), B, Bk = sq, sk, 1, 1
     else:
-        B, Hq, N, d = q.shape
-        Hkv = k.shape[1]
-        same = k.shape[0] == B and k.shape[2] == N
-    if not same:
-        raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)}")
+        raise ValueError("q and k must both be [B, H, N, d] or [total, H, d]")
+    if B != Bk or N != Nk or d != dk:
+        raise ValueError(f"shape mismatch: q {tuple(sq)} k {tuple(sk)}")
     return B, N, Hq, Hkv, d
 
 
-def _rotation(positions, inv_freq, sections, B, N, packed, device):
+def _rows(name, t, shape, index, written=False):
+    """(batch, head, token) strides of a tensor of that shape on that device."""
+    import torch
+    if t.dtype is not torch.bfloat16 or t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor [B, H, N, d] or [total, H, d] on the device of q")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+    s = t.stride()
+    if s[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    # the stride of an axis of one is never used: torch leaves anything there
+    if len(shape) == 4:
+        B, H, N, _ = shape
+        r = (s[0] if B > 1 else 0, s[1] if H > 1 else 0, s[2] if N > 1 else 0)
+    else:
+        B, (N, H, _) = 1, shape
+        r = (0, s[1] if H > 1 else 0, s[0] if N > 1 else 0)
+    if written and 0 in r and any(n > 1 and x == 0 for n, x in zip((B, H, N), r)):
+        raise ValueError(f"{name} is written to and must not be expanded")
+    return r
+
+
+def _rotation(positions, inv_freq, sections, B, N, packed, index):
     """(positions, axis stride, batch stride, inv_freq, sections, axes, rotary_dim) as the C call takes them."""
     import torch
     if inv_freq is None:
         if positions is not None or sections is not None:
             raise ValueError("positions and sections need inv_freq")
         return None, 0, 0, None, None, 0, 0
-    if inv_freq.dtype != torch.float32 or inv_freq.device != device or not inv_freq.is_contiguous() or inv_freq.dim() != 1:
+    if inv_freq.dtype is not torch.float32 or inv_freq.get_device() != index or inv_freq.dim() != 1 or \
+            not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous fp32 CUDA vector on the device of q")
-    half = inv_freq.numel()
-    sections = [half] if sections is None else [int(x) for x in sections]
+    half = inv_freq.shape[0]
+    sections = (half,) if sections is None else [int(x) for x in sections]
     axes = len(sections)
     if not 1 <= axes <= 4 or min(sections) < 0 or sum(sections) != half:
         raise ValueError("sections must be 1 to 4 counts that add up to the length of inv_freq")
     p = positions
-    if p is None or p.dtype != torch.int32 or p.device != device:
+    if p is None or p.dtype is not torch.int32 or p.get_device() != index:
         raise ValueError("positions must be an int32 CUDA tensor on the device of q")
-    want = ([(N,)] if packed else [(N,), (B, N)]) if axes == 1 else []
-    want += [(axes, N)] if packed else [(axes, B, N), (axes, 1, N)]
-    if tuple(p.shape) not in want:
-        raise ValueError(f"positions must be one of {want}, not {tuple(p.shape)}")
-    if N > 1 and p.stride(-1) != 1:
-        raise ValueError("positions must be contiguous along the tokens")
-    if p.dim() == 3:
-        axis, batch = p.stride(0), p.stride(1) if p.shape[1] > 1 else 0
-    elif p.dim() == 2:
-        axis, batch = (p.stride(0), 0) if packed else (0, p.stride(0))
-    else:
+    shape, stride = tuple(p.shape), p.stride()
+    if shape == ((axes, N) if packed else (axes, B, N)):
+        axis, batch = stride[0], 0 if packed or B == 1 else stride[1]
+    elif shape == (axes, 1, N) and not packed:
+        axis, batch = stride[0], 0
+    elif axes == 1 and shape == (N,):
         axis, batch = 0, 0
+    elif axes == 1 and shape == (B, N) and not packed:
+        axis, batch = 0, stride[0]
+    else:
+        raise ValueError(f"positions {shape} do not fit {axes} axes, batch {B} and {N} tokens")
+    if N > 1 and stride[-1] != 1:
+        raise ValueError("positions must be contiguous along the tokens")
     return p.data_ptr(), axis, batch, inv_freq.data_ptr(), (_c_int * axes)(*sections), axes, 2 * half
 
 
-def _weights(q_weight, k_weight, d, device):
+def _weights(q_weight, k_weight, d, index):
+    """1 for bf16 weights, 0 for fp32 or none."""
     import torch
-    if (q_weight is None) != (k_weight is None):
-        raise ValueError("q_weight and k_weight go together")
-    if q_weight is None:
+    if q_weight is None and k_weight is None:
         return 0
-    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if t.dtype not in (torch.float32, torch.bfloat16) or t.device != device or tuple(t.shape) != (d,) or \
-                not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous fp32 or bf16 CUDA vector [{d}] on the device of q")
-    if q_weight.dtype != k_weight.dtype:
+    if q_weight is None or k_weight is None:
+        raise ValueError("q_weight and k_weight go together")
+    dtype = q_weight.dtype
+    if k_weight.dtype is not dtype:
         raise ValueError("q_weight and k_weight must have the same type")
-    return int(q_weight.dtype == torch.bfloat16)
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if (dtype is not torch.float32 and dtype is not torch.bfloat16) or t.get_device() != index or \
+                t.shape != (d,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous fp32 or bf16 CUDA vector [{d}] on the device of q")
+    return int(dtype is torch.bfloat16)
 
 
-def _same_device(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors of a call must be on one device: {t.device} and {device}")
+def _new(t):
+    import torch
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -127,24 +135,16 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
     Returns (q, k) in the shapes of q and k, contiguous unless q_out / k_out say
     otherwise; q_out may be q itself and k_out k (in place).
     """
-    import torch
-    sq, sk = _rows("q", q), _rows("k", k)
     B, N, Hq, Hkv, d = _shapes(q, k)
-    packed = q.dim() == 3
-    rot = _rotation(positions, inv_freq, sections, B, N, packed, q.device)
-    bf16 = _weights(q_weight, k_weight, d, q.device)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-    _same_device(q.device, k, q_out, k_out)
-    strides = sq + sk + _rows("q_out", q_out, q.shape) + _rows("k_out", k_out, k.shape)
-    _written("q_out", q_out)
-    _written("k_out", k_out)
-    with _current_device(q.device):
-        st = lib().attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-                                     (_ll * 12)(*strides), _ptr(q_weight), _ptr(k_weight), bf16, rot[0], rot[1], rot[2],
-                                     rot[3], rot[4], rot[5], rot[6], int(bool(interleaved)), B, N, Hq, Hkv, d,
-                                     float(eps), _stream_handle(q.device))
-    _check(st, "attn_qk_norm_rope")
+    index = q.get_device()
+    strides = _rows("q", q, q.shape, index) + _rows("k", k, k.shape, index)
+    rot = _rotation(positions, inv_freq, sections, B, N, q.dim() == 3, index)
+    bf16 = _weights(q_weight, k_weight, d, index)
+    q_out = _new(q) if q_out is None else q_out
+    k_out = _new(k) if k_out is None else k_out
+    strides += _rows("q_out", q_out, q.shape, index, True) + _rows("k_out", k_out, k.shape, index, True)
+    _call("attn_qk_norm_rope", index, q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _pack12(*strides),
+          _ptr(q_weight), _ptr(k_weight), bf16, *rot, 1 if interleaved else 0, B, N, Hq, Hkv, d, float(eps))
     return q_out, k_out
 
 
@@ -164,35 +164,30 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, positions=None, inv_freq=None, q_weig
         q, k = dq_out, dk_out  # their shapes: nothing of q and k is read
     if q is None or k is None:
         raise ValueError("q and k are needed with a norm")
-    sq, sk = _rows("q", q), _rows("k", k)
     B, N, Hq, Hkv, d = _shapes(q, k)
-    packed = q.dim() == 3
-    rot = _rotation(positions, inv_freq, sections, B, N, packed, q.device)
-    bf16 = _weights(q_weight, k_weight, d, q.device)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
-    _same_device(q.device, k, dq_out, dk_out, dq, dk, workspace)
-    strides = sq + sk + _rows("dq_out", dq_out, q.shape) + _rows("dk_out", dk_out, k.shape) + \
-        _rows("dq", dq, q.shape) + _rows("dk", dk, k.shape)
-    _written("dq", dq)
-    _written("dk", dk)
+    index = q.get_device()
+    strides = _rows("q", q, q.shape, index) + _rows("k", k, k.shape, index)
+    rot = _rotation(positions, inv_freq, sections, B, N, q.dim() == 3, index)
+    bf16 = _weights(q_weight, k_weight, d, index)
+    dq = _new(q) if dq is None else dq
+    dk = _new(k) if dk is None else dk
+    strides += _rows("dq_out", dq_out, q.shape, index) + _rows("dk_out", dk_out, k.shape, index) + \
+        _rows("dq", dq, q.shape, index, True) + _rows("dk", dk, k.shape, index, True)
     dwq = dwk = None
     nbytes = 0
     if norm:
-        dwq, dwk = torch.empty((2, d), dtype=torch.float32, device=q.device)
+        dwq, dwk = (torch.empty(d, dtype=torch.float32, device=q.device) for _ in range(2))
         if workspace is None:
             workspace = torch.empty(int(lib().attn_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hkv, d)),
                                     dtype=torch.uint8, device=q.device)
+        elif workspace.get_device() != index:
+            raise ValueError("workspace must be on the device of q")
         nbytes = workspace.numel() * workspace.element_size()
     else:
         workspace = None
-    with _current_device(q.device):
-        st = lib().attn_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(),
-                                         dk.data_ptr(), (_ll * 18)(*strides), _ptr(q_weight), _ptr(k_weight), bf16,
-                                         _ptr(dwq), _ptr(dwk), rot[0], rot[1], rot[2], rot[3], rot[4], rot[5], rot[6],
-                                         int(bool(interleaved)), B, N, Hq, Hkv, d, float(eps), _ptr(workspace), nbytes,
-                                         _stream_handle(q.device))
-    _check(st, "attn_qk_norm_rope_bwd")
+    _call("attn_qk_norm_rope_bwd", index, q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),
+          dq.data_ptr(), dk.data_ptr(), _pack18(*strides), _ptr(q_weight), _ptr(k_weight), bf16, _ptr(dwq), _ptr(dwk),
+          *rot, 1 if interleaved else 0, B, N, Hq, Hkv, d, float(eps), _ptr(workspace), nbytes)
     return dq, dk, dwq, dwk
 
 
