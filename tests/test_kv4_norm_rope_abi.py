@@ -41,7 +41,7 @@ def _rope(lib, bwd=False, t=None, strides=None, wq=P, wk=P, bf16=0, pos=P, pa=0,
     (dict(eps=float("nan")), 1), (dict(d=80), 2), (dict(d=512), 2), (dict(rot=-16), 1), (dict(rot=144), 1),
     (dict(rot=8, sec=(4,)), 1), (dict(pos=None), 1), (dict(freq=None), 1), (dict(sec=None, axes=1), 1),
     (dict(pa=-1), 1), (dict(pb=-1), 1), (dict(axes=0), 1), (dict(sec=(16, 16, 16, 8, 8)), 1), (dict(sec=(63,)), 1),
-    (dict(sec=(70, -6)), 1), (dict(Hq=70000), 2), (dict(pos=P + 2), 3), (dict(freq=P + 1), 3), (dict(wq=P + 2), 3),
+    (dict(sec=(70, -6)), 1), (dict(Hq=70000), 2), (dict(B=1 << 16, N=1 << 15), 2), (dict(pos=P + 2), 3), (dict(freq=P + 1), 3), (dict(wq=P + 2), 3),
     (dict(wk=P + 1, bf16=1), 3),
 ])
 def test_norm_rope_validation(lib, bwd, kw, code):
