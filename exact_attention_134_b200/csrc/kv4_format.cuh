@@ -60,6 +60,50 @@ __device__ __forceinline__ void kv4_rows(const Kv4Pool& c, int b, int& first, in
   }
 }
 
+// Tiles of 16 tokens that the call's rows lie in. A sequence's n rows touch at
+// most n / 16 + 2 of them, so with the sequences' first rows off[s] the items
+// v(s) = off[s] / 16 + 2 s onwards are its own, and total / 16 + 2 num_seqs
+// items hold them all (rows_per_seq: as many items for each, counted exactly).
+__host__ __device__ __forceinline__ int kv4_items_per_seq(int rows) { return (rows + kKv4Tile - 2) / kKv4Tile + 1; }
+
+__host__ __device__ __forceinline__ long long kv4_num_items(const Kv4Pool& c) {
+  return c.cu == nullptr ? (long long)c.num_seqs * kv4_items_per_seq(c.rows_per_seq)
+                         : c.total / kKv4Tile + 2LL * c.num_seqs;
+}
+
+// One item: the tokens tile * 16 .. + 15 of sequence b, of which the call's are
+// [begin, end) (from token 0 on; possibly none), token j being row first + j.
+struct Kv4Item {
+  int b, tile, begin, end, first;
+};
+
+__device__ __forceinline__ Kv4Item kv4_item(const Kv4Pool& c, int i) {
+  Kv4Item t;
+  int nth;
+  if (c.cu == nullptr) {
+    const int per = kv4_items_per_seq(c.rows_per_seq);
+    t.b = i / per;
+    nth = i - t.b * per;
+  } else {
+    int lo = 0, hi = c.num_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (min(max(__ldg(c.cu + mid), 0), c.total) / kKv4Tile + 2 * mid <= i) lo = mid;
+      else hi = mid - 1;
+    }
+    t.b = lo;
+    nth = i - (min(max(__ldg(c.cu + lo), 0), c.total) / kKv4Tile + 2 * lo);
+  }
+  int row, n;
+  kv4_rows(c, t.b, row, n);
+  const int end = kv4_len(c, t.b), begin = end - n;
+  t.tile = (begin >> 4) + nth;  // tokens below 0 are in tiles below 0
+  t.begin = max(begin, t.tile * kKv4Tile);
+  t.end = min(end, t.tile * kKv4Tile + kKv4Tile);
+  t.first = row - begin;
+  return t;
+}
+
 // The sequence that owns row i: the largest b whose rows begin at or before i.
 __device__ __forceinline__ int kv4_seq_of(const Kv4Pool& c, int i) {
   if (c.cu == nullptr) return i / c.rows_per_seq;

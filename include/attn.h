@@ -455,7 +455,7 @@ ATTN_API attn_status_t attn_qk_norm_rope_bwd(
  * bf16 minimum lo and scale s and 4-bit codes, standing for lo + s * code with
  *     lo = min_c x_c,  s = bf16((max_c x_c - lo) / 15),
  *     code_c = min(rne((x_c - lo) / s), 15).
- * A group with a spread below 15 * 2^-126 is held as its minimum; a group with
+ * A group with a spread below 15 * 2^-125 is held as its minimum; a group with
  * a NaN or an infinity is held as NaN.
  *   pool        device, uint8 [num_pages][Hkv][page_size / 16][20 d],
  *               16-byte aligned; one page is attn_kv4_page_bytes() bytes. The

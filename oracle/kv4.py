@@ -2,7 +2,7 @@
 attention over what the records stand for, in fp64 (integers for codes).
 
 A token's 32 channels x_c of one kv head (bf16): lo = min x, s = bf16((max x -
-lo) / 15), code = min(rne((x - lo) / s), 15); s below 2^-126 is held as 0, a
+lo) / 15), code = min(rne((x - lo) / s), 15); s below 2^-125 is held as 0, a
 group with a NaN or an infinity as s = NaN, lo = 0.
 """
 from __future__ import annotations
@@ -32,7 +32,7 @@ def quantise(bits):
     lo, hi = safe.min(-1), safe.max(-1)
     s = (hi - lo) / 15.0
     sb = np.where(s < 2.0 ** -127, 0, round_bf16(np.maximum(s, 2.0 ** -127))).astype(np.uint16)
-    sb = np.where(sb < 0x0080, 0, sb).astype(np.uint16)
+    sb = np.where(sb < 0x0100, 0, sb).astype(np.uint16)
     scale = widen_bf16(sb).astype(np.float64)
     q = np.divide(safe - lo[..., None], scale[..., None], out=np.zeros_like(safe), where=scale[..., None] > 0)
     codes = np.minimum(np.rint(q), 15).astype(np.uint8)

@@ -62,9 +62,12 @@ def _filled(lens, H, d, page, seed):
 
 @pytest.mark.parametrize("d,page,Hkv", [(64, 16, 1), (96, 32, 3), (128, 64, 2), (256, 1024, 1), (128, 16, 5)])
 @pytest.mark.parametrize("ragged", [False, True])
-def test_append_writes_the_new_tokens_and_nothing_else(d, page, Hkv, ragged):
+@pytest.mark.parametrize("many", [False, True])
+def test_append_writes_the_new_tokens_and_nothing_else(d, page, Hkv, ragged, many):
     g = torch.Generator().manual_seed(d + page)
     lens, new = ([5, 40, 33, 16], [5, 17, 0, 3]) if ragged else ([20, 4, 33], [3, 3, 3])
+    if many:  # whole records
+        lens, new = ([70, 100, 33, 200, 16], [40, 100, 0, 137, 16]) if ragged else ([64, 50, 91], [48, 48, 48])
     rows, pages = _table(lens, page, g)
     pool = torch.randint(0, 256, (pages, Hkv, page // 16, 20 * d), generator=g, dtype=torch.uint8)
     total = sum(new)
@@ -109,17 +112,41 @@ def test_append_writes_the_new_tokens_and_nothing_else(d, page, Hkv, ragged):
     assert (ko[t:] == 7).all() and (vo[t:] == 7).all()     # rows that no sequence owns
 
 
-def test_append_of_more_tokens_than_cached_and_gather_before_the_first():
+@pytest.mark.parametrize("n", [5, 37])
+def test_append_of_more_tokens_than_cached_and_gather_before_the_first(n):
     g = torch.Generator().manual_seed(3)
-    pool = torch.randint(0, 256, (4, 2, 1, 20 * 64), generator=g, dtype=torch.uint8).cuda()
-    k, v = (x.cuda() for x in _keys_values(10, 2, 64, g))
+    pool = torch.randint(0, 256, (4, 2, 4, 20 * 64), generator=g, dtype=torch.uint8).cuda()
+    k, v = (x.cuda() for x in _keys_values(2 * n, 2, 64, g))
     a, b = pool.clone(), pool.clone()
-    attn.kv4_append(k, v, a, _ints([[1], [3]]), _ints([3, 5]))             # 5 rows each: two are before token 0
-    attn.kv4_append(k[2:], v[2:], b, _ints([[1], [3]]), _ints([3, 5]), _ints([0, 3, 8]))
+    attn.kv4_append(k, v, a, _ints([[1], [3]]), _ints([3, n]))             # n rows each: n - 3 are before token 0
+    attn.kv4_append(k[n - 3:], v[n - 3:], b, _ints([[1], [3]]), _ints([3, n]), _ints([0, 3, n + 3]))
     assert torch.equal(a, b)
-    ko, vo = attn.kv4_gather(a, _ints([[1], [3]]), _ints([3, 0]), 8)
-    assert not ko[0].any() and not ko[4:].any() and not vo[4:].any() and ko[1:4].any()
+    ko, vo = attn.kv4_gather(a, _ints([[1], [3]]), _ints([3, 0]), 2 * n - 2)
+    assert not ko[:n - 4].any() and ko[n - 4:n - 1].any(-1).all() and not ko[n - 1:].any() and not vo[n - 1:].any()
+    whole, _ = attn.kv4_gather(a, _ints([[1], [3]]), _ints([3, n]), n + 3, _ints([0, 3, n + 3]))
+    assert torch.equal(whole[:3], ko[n - 4:n - 1])
     assert attn.get_status()[0] == 0
+
+
+def test_ties_of_the_quantiser_go_to_even():
+    """Quotients of a half exactly, for every scale of 8 bits: codes k and k + 1 are as near, the even one is held."""
+    m = torch.arange(128, 256).float()                                  # scales m * 2^-9
+    x = torch.zeros(128, 1, 64)
+    x[:, 0, 15] = 15 * m                                                # max, min 0: a span of 15 scales
+    x[:, 0, 1:15] = (torch.arange(14) + 0.5) * m[:, None]
+    x = x * 2.0 ** -9
+    x[:, 0, 32:] = -x[:, 0, :32]
+    b = x.bfloat16()
+    rows = [[0, 1]]
+    want = np.zeros((2, 1, 4, 20 * 64), np.uint8)
+    bits = bf16_bits(b)
+    for j in range(128):
+        kv4.write_token(want[j // 64, 0, j // 16 % 4], j % 16, bits[j, 0], bits[j, 0])
+    for new in (128, 1):  # whole records, then single rows
+        pool = torch.zeros((2, 1, 4, 20 * 64), dtype=torch.uint8, device="cuda")
+        for at in range(0, 128, new):
+            attn.kv4_append(b[at:at + new].cuda(), b[at:at + new].cuda(), pool, _ints(rows), _ints([at + new]))
+        assert np.array_equal(pool.cpu().numpy(), want)
 
 
 def test_lengths_are_clamped_to_the_table_and_bad_pages_reported():
