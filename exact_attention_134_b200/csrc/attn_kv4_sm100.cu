@@ -45,9 +45,11 @@ namespace attn_sm100 {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr float kNone = -3.0e38f;  // reference of a row that has seen no key
-constexpr int kMinScale = -64;       // smaller scales count as 2^-64: p stays below 2^79
-constexpr float kHead = 8.0f;      // log2 of p * s at the reference: 2^7 of room before the next rescale
+constexpr float kNone = -3.0e38f;     // reference of a row that has seen no key
+constexpr uint32_t kMinScale = 0x1f80u;  // bf16 2^-64: smaller scales count as that, so p stays below 2^79
+constexpr float kRoom = 32768.0f;     // p * s stays below 2^15
+constexpr float kHead = 8.0f;         // log2 of p * s at a new reference: 2^7 of room before the next one
+constexpr int kPair = 2;              // records of a step
 
 struct Kv4Params {
   Kv4Pool c;
@@ -69,11 +71,12 @@ template <int D, int NT>
 struct Kv4Cfg {
   static constexpr int kWarps = (NT == 1 && D <= 128) ? 8 : 4;
   static constexpr int kCtasPerSm = NT == 2 && D == 64 ? 3 : 2;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = 2;
   static constexpr int kCols = 8 * NT;
   static constexpr int kRecord = kv4_record_bytes(D);
-  static constexpr int kRing = kWarps * kStages * kRecord;
-  static constexpr int kJoin = kWarps * kCols * D * 4;        // fp32 O of every warp
+  static constexpr int kStage = kPair * kRecord;
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kJoin = kWarps / 2 * kCols * D * 4;    // fp32 O of half the warps
   static constexpr int kRl = 2 * kWarps * kCols * 8;          // (reference, sum), two segments
   static constexpr int kBars = kWarps * kStages * 8;
   static constexpr int kSmemBytes = kRing + kJoin + kRl + kBars + 16;
@@ -90,6 +93,13 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a2
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %5}, {%7, %8}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_bf16_full(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // 8 x 8 transposition of 16-bit values over the warp.
@@ -138,8 +148,8 @@ __device__ __forceinline__ uint32_t lds_word(uint32_t addr) {
 }
 
 // A sequence's part in the list of units: `blocks` row blocks for each kv
-// head, `units` for each of those (one per record; one also for an empty
-// cache, so that its rows get their result).
+// head, `units` for each of those (one per pair of records; one also for an
+// empty cache, so that its rows get their result).
 struct SeqWork {
   int first, n, len, blocks, units;
 };
@@ -149,7 +159,7 @@ __device__ __forceinline__ SeqWork seq_work(const Kv4Params& p, int b) {
   kv4_rows(p.c, b, s.first, s.n);
   s.len = kv4_len(p.c, b);
   s.blocks = (int)(((long long)s.n * p.group + COLS - 1) / COLS);
-  s.units = max(1, (s.len + kKv4Tile - 1) / kKv4Tile);
+  s.units = max(1, (s.len + kPair * kKv4Tile - 1) / (kPair * kKv4Tile));
   return s;
 }
 
@@ -220,12 +230,13 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
     attn_kv4_kernel(const __grid_constant__ Kv4Params p) {
   using C = Kv4Cfg<D, NT>;
   constexpr int W = C::kWarps, S = C::kStages, G = D / 32, COLS = C::kCols;
+  constexpr int MINS = (G + 3) / 4;  // instructions for the minima of a record
   extern __shared__ __align__(128) uint8_t smem[];
   float* const join = reinterpret_cast<float*>(smem + C::kRing);
   float2* const rl = reinterpret_cast<float2*>(smem + C::kRing + C::kJoin);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + C::kRing + C::kJoin + C::kRl + C::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
-  const uint32_t ring = smem_addr(smem) + warp * S * C::kRecord;
+  const uint32_t ring = smem_addr(smem) + warp * S * C::kStage;
   const uint32_t bars = smem_addr(smem + C::kRing + C::kJoin + C::kRl) + warp * S * 8;
 
   if (lane == 0) {
@@ -266,51 +277,65 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
   }
   if (!any) return;
 
-  // ---- the ring: this warp's records, over all segments of the range
+  // ---- the ring: this warp's units, over all segments of the range
+  int flying = 0;         // stages on their way
   Segment pf = seg;
   long long pf_left = end - begin;
-  pf.t1 = (int)min((long long)pf.s.units, pf.t0 + pf_left);
-  int pf_k = 0;           // next record of the warp in pf: unit t0 + warp + W * pf_k
-  int pf_pages = 0;       // page of record (pf_k / 32) * 32 + lane
-  bool pf_more = true;
-  unsigned issued = 0, taken = 0;
-  uint32_t bad = 0;       // bit s: the record of stage s is on no page of the pool
-
-  auto records = [&](const Segment& g) {  // of this warp in segment g
-    const int e = min(g.t1, (g.s.len + kKv4Tile - 1) / kKv4Tile);
-    return max(0, (e - g.t0 - warp + W - 1) / W);
+  auto units = [&](const Segment& g) {  // of this warp in segment g (none of an empty cache)
+    return g.s.len > 0 ? max(0, (g.t1 - g.t0 - warp + W - 1) / W) : 0;
   };
+  pf.t1 = (int)min((long long)pf.s.units, pf.t0 + pf_left);
+  int pf_k = 0, pf_count = units(pf);  // next unit of the warp in pf (t0 + warp + W * pf_k), and how many
+  int pf_pages[kPair];    // pages of the records of unit (pf_k / 32) * 32 + lane
+  int pf_stage = 0;
+  bool pf_more = true;
+  uint32_t bad = 0;       // bits kPair * stage + i: record i of the stage is on no page of the pool
+
   auto issue = [&]() {
-    while (pf_more && pf_k >= records(pf)) {
+    while (pf_k >= pf_count) {
+      if (!pf_more) return;
       pf_left -= pf.t1 - pf.t0;
       pf_more = pf_left > 0 && next_segment<COLS>(p, pf);
-      if (pf_more) pf.t1 = (int)min((long long)pf.s.units, pf_left);
+      if (!pf_more) return;
+      pf.t1 = (int)min((long long)pf.s.units, pf_left);
       pf_k = 0;
+      pf_count = units(pf);
     }
-    if (!pf_more) return;
     if ((pf_k & 31) == 0) {
-      const int t = pf.t0 + warp + W * (pf_k + lane);
-      pf_pages = t < pf.t1 && t * kKv4Tile < pf.s.len
-                     ? __ldg(p.c.table + (size_t)pf.b * p.c.max_pages + (t >> p.c.tiles_log2))
-                     : -1;
+      const int t = kPair * (pf.t0 + warp + W * (pf_k + lane));
+#pragma unroll
+      for (int i = 0; i < kPair; ++i)
+        pf_pages[i] = pf_k + lane < pf_count && (t + i) * kKv4Tile < pf.s.len
+                          ? __ldg(p.c.table + (size_t)pf.b * p.c.max_pages + ((t + i) >> p.c.tiles_log2))
+                          : -1;
     }
-    const int page = __shfl_sync(kFull, pf_pages, pf_k & 31);
-    const int t = pf.t0 + warp + W * pf_k;
-    const int st = issued % S;
-    const bool ok = page >= 0 && page < p.c.num_pages;
-    bad = ok ? bad & ~(1u << st) : bad | (1u << st);
+    const int t = kPair * (pf.t0 + warp + W * pf_k);
+    const uint32_t bar = bars + 8 * pf_stage, to = ring + pf_stage * C::kStage;
+    int page[kPair];
+#pragma unroll
+    for (int i = 0; i < kPair; ++i) page[i] = __shfl_sync(kFull, pf_pages[i], pf_k & 31);
+    const bool two = (t + 1) * kKv4Tile < pf.s.len;
+    const bool ok0 = (unsigned)page[0] < (unsigned)p.c.num_pages, ok1 = two && (unsigned)page[1] < (unsigned)p.c.num_pages;
+    const uint32_t b0 = (ok0 ? 0u : 1u) | (two && !ok1 ? 2u : 0u);
+    bad = (bad & ~(3u << (kPair * pf_stage))) | b0 << (kPair * pf_stage);
     if (lane == 0) {
-      if (ok) {
-        mbar_arrive_expect_tx(bars + 8 * st, C::kRecord);
-        bulk_load(ring + st * C::kRecord,
-                  p.c.data + kv4_record(p.c, page, pf.h, t & ((1 << p.c.tiles_log2) - 1), D), C::kRecord, bars + 8 * st);
+      const int mask = (1 << p.c.tiles_log2) - 1;
+      const uint8_t* const from = p.c.data + kv4_record(p.c, page[0], pf.h, t & mask, D);
+      if (b0 == 0 && two && mask != 0) {  // both in one page: side by side
+        mbar_arrive_expect_tx(bar, C::kStage);
+        bulk_load(to, from, C::kStage, bar);
       } else {
-        mbar_arrive(bars + 8 * st);
-        kv4_bad_page(p.status, 0x500);
+        const uint32_t n = (ok0 ? 1u : 0u) + (ok1 ? 1u : 0u);
+        if (n) mbar_arrive_expect_tx(bar, n * C::kRecord);
+        else mbar_arrive(bar);
+        if (ok0) bulk_load(to, from, C::kRecord, bar);
+        if (ok1) bulk_load(to + C::kRecord, p.c.data + kv4_record(p.c, page[1], pf.h, (t + 1) & mask, D), C::kRecord, bar);
+        if (b0) kv4_bad_page(p.status, 0x500);
       }
     }
-    ++issued;
+    pf_stage = pf_stage + 1 == S ? 0 : pf_stage + 1;
     ++pf_k;
+    ++flying;
   };
 #pragma unroll 1
   for (int i = 0; i < S; ++i) issue();
@@ -318,11 +343,14 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
   long long left = end - begin;
   seg.t1 = (int)min((long long)seg.s.units, seg.t0 + left);
   bool ok = true;
+  int stage = 0;
+  uint32_t phase = 0;
   int turn = 0;  // parity of the segment, for rl
   while (true) {
     // ---- query rows of the segment, as operands
     uint32_t qf[NT][G][4];
-    float qsum[NT][G][2], fac[NT][2];
+    uint32_t qmin[NT][MINS][2];  // sums over the groups, for the minima: three bf16 pieces of each
+    float fac[NT][2];
     int limit[NT][2];  // last key that the lane's two columns see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -346,32 +374,37 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
       // codes that stand 4 bits up, still is a normal number down to 2^-24 of it
       const int k = min(max(13 - ((int)(top >> 7) - 127), -90), 100);
       const float up = __uint_as_float((uint32_t)(k + 127) << 23);
-      float sum[G];
+      float mine = 0.0f, other = 0.0f;  // the sums over groups t4 and t4 + 4
 #pragma unroll
       for (int gr = 0; gr < G; ++gr) {
         const uint32_t w[4] = {raw[gr].x, raw[gr].y, raw[gr].z, raw[gr].w};
-        float f[8];
-        sum[gr] = 0.0f;
+        float f[8], sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           f[i] = (i % 2 ? hi16(w[i / 2]) : lo16(w[i / 2])) * up;
-          sum[gr] += f[i];
+          sum += f[i];
         }
         // codes i and i + 4 share a register; 1, 3, 5, 7 stand 4 bits up
         qf[nt][gr][0] = pack_f16x2(f[0], f[4]);
         qf[nt][gr][1] = pack_f16x2(f[1] * 0.0625f, f[5] * 0.0625f);
         qf[nt][gr][2] = pack_f16x2(f[2], f[6]);
         qf[nt][gr][3] = pack_f16x2(f[3] * 0.0625f, f[7] * 0.0625f);
-        sum[gr] += __shfl_xor_sync(kFull, sum[gr], 1);
-        sum[gr] += __shfl_xor_sync(kFull, sum[gr], 2);
+        sum += __shfl_xor_sync(kFull, sum, 1);
+        sum += __shfl_xor_sync(kFull, sum, 2);
+        if (t4 == gr % 4) (gr < 4 ? mine : other) = sum * 5.9604644775390625e-8f;  // 2^-24
       }
-      const float back = p.scale_log2 * __uint_as_float((uint32_t)(24 - k + 127) << 23);
+#pragma unroll
+      for (int m = 0; m < MINS; ++m) {
+        const float s = m ? other : mine;
+        const float h = hi16(__float_as_uint(s)), l = hi16(__float_as_uint(s - h));
+        qmin[nt][m][0] = pack_bf16x2(h, l);
+        qmin[nt][m][1] = pack_bf16x2((s - h) - l, 0.0f);
+      }
+      // above 0, for the product with a masked score
+      const float back = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(24 - k + 127) << 23), 1.17549435e-38f);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {  // the lane's columns 2 t4 + j
-        const int from = 4 * (2 * t4 + j);
-#pragma unroll
-        for (int gr = 0; gr < G; ++gr) qsum[nt][gr][j] = __shfl_sync(kFull, sum[gr], from) * 5.9604644775390625e-8f;  // 2^-24
-        fac[nt][j] = __shfl_sync(kFull, back, from);
+        fac[nt][j] = __shfl_sync(kFull, back, 4 * (2 * t4 + j));
         const int r = seg.rb * COLS + nt * 8 + 2 * t4 + j;
         limit[nt][j] = p.causal ? seg.s.len - seg.s.n + min(r / p.group, seg.s.n - 1) : seg.s.len - 1;
       }
@@ -392,116 +425,117 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
       sum[nt][0] = sum[nt][1] = 0.0f;
     }
 
-    const int mine = records(seg);
+    const int mine = units(seg);
+    int key = (seg.t0 + warp) * kPair * kKv4Tile + g8;  // the lane's keys: key + 8 i
 #pragma unroll 1
-    for (int k = 0; k < mine && ok; ++k) {
-      const int st = taken % S;
-      ok = __all_sync(kFull, bounded_wait(bars + 8 * st, (taken / S) & 1u, abort_flag, p.timeout_ns));
+    for (int k = 0; k < mine; ++k, key += W * kPair * kKv4Tile) {
+      ok = ok && __all_sync(kFull, bounded_wait(bars + 8 * stage, phase, abort_flag, p.timeout_ns));
       if (!ok) break;
-      ++taken;
-      if (bad >> st & 1u) {
-        issue();
-        continue;
-      }
-      const int key = (seg.t0 + warp + W * k) * kKv4Tile + g8;  // the lane's keys: key and key + 8
-      const bool edge = key - g8 + kKv4Tile - 1 > all_see;
-      const uint32_t rec = ring + st * C::kRecord;
+      --flying;
+      const uint32_t rec = ring + stage * C::kStage;
+      const uint32_t lost = bad >> (kPair * stage) & 3u;
+      const bool edge = key - g8 + kPair * kKv4Tile - 1 > all_see || lost != 0;
 
-      // ---- scores
-      float x[NT][4];
+      // ---- scores, against the reference
+      float x[kPair][NT][4];
+      uint32_t vs[kPair][G];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[nt][i] = 0.0f;
-      {
-        uint32_t ks[G], kl[G];
-        lds_words<G>(ks, rec + 16 * D + g8 * G * 4);
-        lds_words<G>(kl, rec + 17 * D + g8 * G * 4);
-#pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-          uint32_t w0, w1;
-          lds_pair(w0, w1, rec + gr * 256 + lane * 8);
-          const float s0 = lo16(ks[gr]), s1 = hi16(ks[gr]), m0 = lo16(kl[gr]), m1 = hi16(kl[gr]);
-          float acc[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
-            mma_f16(acc[nt], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, qf[nt][gr][0],
-                    qf[nt][gr][1]);
-            mma_f16(acc[nt], (w0 >> 8) & 0x000f000fu, (w1 >> 8) & 0x000f000fu, (w0 >> 8) & 0x00f000f0u,
-                    (w1 >> 8) & 0x00f000f0u, qf[nt][gr][2], qf[nt][gr][3]);
-            x[nt][0] = fmaf(m0, qsum[nt][gr][0], fmaf(s0, acc[nt][0], x[nt][0]));
-            x[nt][1] = fmaf(m0, qsum[nt][gr][1], fmaf(s0, acc[nt][1], x[nt][1]));
-            x[nt][2] = fmaf(m1, qsum[nt][gr][0], fmaf(s1, acc[nt][2], x[nt][2]));
-            x[nt][3] = fmaf(m1, qsum[nt][gr][1], fmaf(s1, acc[nt][3], x[nt][3]));
-          }
-        }
-      }
-      // ---- the rest of the record, then its stage is free
-      uint32_t vw[G][2], vs[G], vm[2];
-      lds_words<G>(vs, rec + 18 * D + g8 * G * 4);
-#pragma unroll
-      for (int gr = 0; gr < G; ++gr) lds_pair(vw[gr][0], vw[gr][1], rec + 8 * D + gr * 256 + lane * 8);
-      vm[0] = g8 < G ? lds_word(rec + 19 * D + g8 * 32 + t4 * 4) : 0u;
-      vm[1] = g8 < G ? lds_word(rec + 19 * D + g8 * 32 + 16 + t4 * 4) : 0u;
-      __syncwarp();
-      issue();
-
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[nt][i] *= fac[nt][i & 1];
-      if (edge) {
-        // keys behind the cached ones hold anything: no scale or minimum of
-        // theirs counts; keys that a row does not see get -inf
-        const uint32_t keep = (key < seg.s.len ? 0x0000ffffu : 0u) | (key + 8 < seg.s.len ? 0xffff0000u : 0u);
-        const int pair = key - g8 + 2 * t4;
-#pragma unroll
-        for (int gr = 0; gr < G; ++gr) vs[gr] &= keep;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          vm[i] &= (pair + 8 * i < seg.s.len ? 0x0000ffffu : 0u) | (pair + 8 * i + 1 < seg.s.len ? 0xffff0000u : 0u);
+      for (int i = 0; i < kPair; ++i) {
+        const uint32_t r = rec + i * C::kRecord;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (key + (i & 2) * 4 > limit[nt][i & 1]) x[nt][i] = -INFINITY;
-      }
-      // ---- the largest V scale of the record is below 2^e; so is a 2^-48th of
-      // its minima, whose products with p would overflow behind smaller ones
-      // (and need no codes: the minima's weights hold 16 bits)
-      uint32_t top = 0, vtop = __vmaxu2(vm[0] & 0x7fff7fffu, vm[1] & 0x7fff7fffu);
-      vtop = max(vtop & 0xffffu, vtop >> 16);
-      vtop = vtop > (48u << 7) ? vtop - (48u << 7) : 0u;
+          for (int e = 0; e < 4; ++e) x[i][nt][e] = 0.0f;
+        // the minima of key g8 (+ 8) and group t4: once for each of two pieces of the sums
 #pragma unroll
-      for (int gr = 0; gr < G; ++gr) top = __vmaxu2(top, vs[gr] & 0x7fff7fffu);
-      top = __reduce_max_sync(kFull, max(max(top & 0xffffu, top >> 16), vtop));
-      if (top >= 0x7f80u) {  // NaN groups: of no weight in the choice of the reference
-        top = vtop;
+        for (int m = 0; m < MINS; ++m) {
+          const uint32_t kl = 4 * m + t4 < G ? lds_word(r + 17 * D + (g8 * G + 4 * m + t4) * 4) : 0u;
+          const uint32_t a0 = __byte_perm(kl, kl, 0x1010), a1 = __byte_perm(kl, kl, 0x3232);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_bf16_full(x[i][nt], a0, a1, a0, a1, qmin[nt][m][0], qmin[nt][m][1]);
+        }
+        uint32_t ks[G];
+        lds_words<G>(ks, r + 16 * D + g8 * G * 4);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
-          const uint32_t a = vs[gr] & 0x7fffu, b = (vs[gr] >> 16) & 0x7fffu;
-          top = max(top, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
+          uint32_t w0, w1;
+          lds_pair(w0, w1, r + gr * 256 + lane * 8);
+          const float s0 = lo16(ks[gr]), s1 = hi16(ks[gr]);
+          const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma_f16(acc, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, qf[nt][gr][0],
+                    qf[nt][gr][1]);
+            mma_f16(acc, v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u, qf[nt][gr][2],
+                    qf[nt][gr][3]);
+            x[i][nt][0] = fmaf(s0, acc[0], x[i][nt][0]);
+            x[i][nt][1] = fmaf(s0, acc[1], x[i][nt][1]);
+            x[i][nt][2] = fmaf(s1, acc[2], x[i][nt][2]);
+            x[i][nt][3] = fmaf(s1, acc[3], x[i][nt][3]);
+          }
         }
-        top = __reduce_max_sync(kFull, top);
+        lds_words<G>(vs[i], r + 18 * D + g8 * G * 4);
       }
-      const float e = (float)max((int)(top >> 7) - 126, kMinScale);
-      // ---- a new reference where p * s would pass 2^15
+      if (edge) {
+        // keys behind the cached ones hold anything: no scale of theirs counts;
+        // keys that a row does not see get -inf
+#pragma unroll
+        for (int i = 0; i < kPair; ++i) {
+          const int at = key + kKv4Tile * i, len = lost >> i & 1u ? 0 : seg.s.len;
+          const uint32_t keep = (at < len ? 0x0000ffffu : 0u) | (at + 8 < len ? 0xffff0000u : 0u);
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr) vs[i][gr] &= keep;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (at + (e & 2) * 4 > limit[nt][e & 1] || !(keep >> (e & 2) * 8 & 1u)) x[i][nt][e] = -INFINITY;
+        }
+      }
+      // ---- weights; a new reference where p * s would pass 2^15. The bound of s
+      // is each key's own, over its groups
+      float pr[kPair][NT][4];
       bool over = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int i = 0; i < kPair; ++i) {
+        uint32_t top = kMinScale | kMinScale << 16;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) over |= fmaxf(x[nt][j], x[nt][2 + j]) - ref[nt][j] > 15.0f - e;
+        for (int gr = 0; gr < G; ++gr) top = __vmaxu2(top, vs[i][gr]);
+        const float s0 = lo16(top), s1 = hi16(top);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pr[i][nt][e] = ex2_approx(fmaf(x[i][nt][e], fac[nt][e & 1], -ref[nt][e & 1]));
+          const float m0 = fmaxf(pr[i][nt][0], pr[i][nt][1]) * s0, m1 = fmaxf(pr[i][nt][2], pr[i][nt][3]) * s1;
+          over |= !(m0 < kRoom) || !(m1 < kRoom);  // NaN scales too
+        }
+      }
       if (__any_sync(kFull, over)) {
+        float bound[kPair][2];  // log2 of the keys' scales, NaN ones left out
+#pragma unroll
+        for (int i = 0; i < kPair; ++i) {
+          uint32_t t0 = kMinScale, t1 = kMinScale;
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr) {
+            const uint32_t a = vs[i][gr] & 0xffffu, b = vs[i][gr] >> 16;
+            t0 = max(t0, a < 0x7f80u ? a : 0u);
+            t1 = max(t1, b < 0x7f80u ? b : 0u);
+          }
+          bound[i][0] = (float)((int)(t0 >> 7) - 126);
+          bound[i][1] = (float)((int)(t1 >> 7) - 126);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float m = fmaxf(x[nt][j], x[nt][2 + j]);
+            float m = kNone;
+#pragma unroll
+            for (int i = 0; i < kPair; ++i)
+              m = fmaxf(m, fmaxf(fmaf(x[i][nt][j], fac[nt][j], bound[i][0]), fmaf(x[i][nt][2 + j], fac[nt][j], bound[i][1])));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-            const float next = fmaxf(ref[nt][j], m + (e - kHead));
+            const float next = fmaxf(ref[nt][j], m - kHead);
             const float f = ex2_approx(ref[nt][j] - next);
             ref[nt][j] = next;
             sum[nt][j] *= f;
@@ -511,41 +545,67 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
               o[nt][q][2 + j] *= f;
             }
             omin[nt][j] *= f;
+#pragma unroll
+            for (int i = 0; i < kPair; ++i) {
+              pr[i][nt][j] = ex2_approx(fmaf(x[i][nt][j], fac[nt][j], -next));
+              pr[i][nt][2 + j] = ex2_approx(fmaf(x[i][nt][2 + j], fac[nt][j], -next));
+            }
           }
       }
       // ---- O^T += V^T P^T
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float pr[4];
+      for (int i = 0; i < kPair; ++i) {
+        const uint32_t r = rec + i * C::kRecord;
+        uint32_t vm[2];
+        vm[0] = g8 < G ? lds_word(r + 19 * D + g8 * 32 + t4 * 4) : 0u;
+        vm[1] = g8 < G ? lds_word(r + 19 * D + g8 * 32 + 16 + t4 * 4) : 0u;
+        if (edge) {
+          const int pair = key - g8 + kKv4Tile * i + 2 * t4, len = lost >> i & 1u ? 0 : seg.s.len;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pr[i] = ex2_approx(x[nt][i] - ref[nt][i & 1]);
-        sum[nt][0] += pr[0] + pr[2];
-        sum[nt][1] += pr[1] + pr[3];
-        {
+          for (int e = 0; e < 2; ++e)
+            vm[e] &= (pair + 8 * e < len ? 0x0000ffffu : 0u) | (pair + 8 * e + 1 < len ? 0xffff0000u : 0u);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float(&pe)[4] = pr[i][nt];
+          sum[nt][0] += pe[0] + pe[2];
+          sum[nt][1] += pe[1] + pe[3];
           // the minimum's weights in two bf16 steps (16 bits): the minimum and
           // the codes' part cancel, so a single one would show in the result
-          const uint32_t h0 = __byte_perm(__float_as_uint(pr[0]), __float_as_uint(pr[1]), 0x7632);
-          const uint32_t h1 = __byte_perm(__float_as_uint(pr[2]), __float_as_uint(pr[3]), 0x7632);
-          const uint32_t l0 = pack_bf16x2(pr[0] - lo16(h0), pr[1] - hi16(h0));
-          const uint32_t l1 = pack_bf16x2(pr[2] - lo16(h1), pr[3] - hi16(h1));
+          const uint32_t h0 = __byte_perm(__float_as_uint(pe[0]), __float_as_uint(pe[1]), 0x7632);
+          const uint32_t h1 = __byte_perm(__float_as_uint(pe[2]), __float_as_uint(pe[3]), 0x7632);
+          const uint32_t l0 = pack_bf16x2(pe[0] - lo16(h0), pe[1] - hi16(h0));
+          const uint32_t l1 = pack_bf16x2(pe[2] - lo16(h1), pe[3] - hi16(h1));
           mma_bf16(omin[nt], vm[0], vm[1], transpose8(h0), transpose8(h1));
           mma_bf16(omin[nt], vm[0], vm[1], transpose8(l0), transpose8(l1));
         }
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
-          const float s0 = lo16(vs[gr]), s1 = hi16(vs[gr]);
-          float w[4] = {pr[0] * s0, pr[1] * s0, pr[2] * s1, pr[3] * s1};
-          if (edge) {  // a NaN group reaches only the rows that see its key
+          uint32_t a, b;
+          lds_pair(a, b, r + 8 * D + gr * 256 + lane * 8);
+          const float s0 = lo16(vs[i][gr]), s1 = hi16(vs[i][gr]);
+          const uint32_t a8 = a >> 8, b8 = b >> 8;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (x[nt][i] == -INFINITY) w[i] = 0.0f;
+          for (int nt = 0; nt < NT; ++nt) {
+            const float(&pe)[4] = pr[i][nt];
+            float w[4] = {pe[0] * s0, pe[1] * s0, pe[2] * s1, pe[3] * s1};
+            if (edge) {  // a NaN group reaches only the rows that see its key
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (x[i][nt][e] == -INFINITY) w[e] = 0.0f;
+            }
+            const uint32_t p0 = transpose8(pack_f16x2(w[0], w[1])), p1 = transpose8(pack_f16x2(w[2], w[3]));
+            mma_f16(o[nt][2 * gr], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u, p0, p1);
+            mma_f16(o[nt][2 * gr + 1], a8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x000f000fu, b8 & 0x00f000f0u, p0, p1);
           }
-          const uint32_t b0 = transpose8(pack_f16x2(w[0], w[1])), b1 = transpose8(pack_f16x2(w[2], w[3]));
-          const uint32_t a = vw[gr][0], b = vw[gr][1];
-          mma_f16(o[nt][2 * gr], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u, b0, b1);
-          mma_f16(o[nt][2 * gr + 1], (a >> 8) & 0x000f000fu, (a >> 8) & 0x00f000f0u, (b >> 8) & 0x000f000fu,
-                  (b >> 8) & 0x00f000f0u, b0, b1);
         }
+      }
+      // ---- the stage is free
+      __syncwarp();
+      issue();
+      if (++stage == S) {
+        stage = 0;
+        phase ^= 1u;
       }
     }
     if (!ok && lane == 0) {
@@ -564,26 +624,37 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
         if (g8 == 0) my_rl[warp * COLS + nt * 8 + 2 * t4 + j] = make_float2(ref[nt][j], sum[nt][j]);
       }
     __syncthreads();
+    // O of the upper half of the warps, then the lower half's added to it
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int half = 1; half >= 0; --half) {
+      if (warp / (W / 2) == half) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int col = nt * 8 + 2 * t4 + j;
-        float top = my_rl[col].x;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int w = 1; w < W; ++w) top = fmaxf(top, my_rl[w * COLS + col].x);
-        const float f = ex2_approx(ref[nt][j] - top);
-        const float f0 = f * 16777216.0f, f1 = f * 1048576.0f;  // 2^24, and a sixteenth of it
-        float* const to = join + (warp * COLS + col) * D + 4 * g8;
+          for (int j = 0; j < 2; ++j) {
+            const int col = nt * 8 + 2 * t4 + j;
+            float top = my_rl[col].x;
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-          const float lo = f * __shfl_sync(kFull, omin[nt][j], gr * 4 + t4);
-          *reinterpret_cast<float4*>(to + 32 * gr) =
-              make_float4(fmaf(f0, o[nt][2 * gr][j], lo), fmaf(f1, o[nt][2 * gr][2 + j], lo),
-                          fmaf(f0, o[nt][2 * gr + 1][j], lo), fmaf(f1, o[nt][2 * gr + 1][2 + j], lo));
-        }
+            for (int w = 1; w < W; ++w) top = fmaxf(top, my_rl[w * COLS + col].x);
+            const float f = ex2_approx(ref[nt][j] - top);
+            const float f0 = f * 16777216.0f, f1 = f * 1048576.0f;  // 2^24, and a sixteenth of it
+            float* const to = join + (warp % (W / 2) * COLS + col) * D + 4 * g8;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+              const float lo = f * __shfl_sync(kFull, omin[nt][j], gr * 4 + t4);
+              float4 v = make_float4(fmaf(f0, o[nt][2 * gr][j], lo), fmaf(f1, o[nt][2 * gr][2 + j], lo),
+                                     fmaf(f0, o[nt][2 * gr + 1][j], lo), fmaf(f1, o[nt][2 * gr + 1][2 + j], lo));
+              float4* const at = reinterpret_cast<float4*>(to + 32 * gr);
+              if (half == 0) {
+                const float4 u = *at;
+                v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+              }
+              *at = v;
+            }
+          }
       }
-    __syncthreads();
+      __syncthreads();
+    }
     const bool whole = seg.t0 == 0 && seg.t1 == seg.s.units;
     const size_t slot = 2 * (size_t)blockIdx.x + (seg.t0 > 0 ? 0 : 1);
     for (int i = threadIdx.x; i < COLS * (D / 4); i += W * 32) {
@@ -594,14 +665,15 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
       for (int w = 1; w < W; ++w) top = fmaxf(top, my_rl[w * COLS + col].x);
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
+      for (int w = 0; w < W / 2; ++w) {
         const float4 v = reinterpret_cast<const float4*>(join + (w * COLS + col) * D)[c4];
         a.x += v.x;
         a.y += v.y;
         a.z += v.z;
         a.w += v.w;
-        l += my_rl[w * COLS + col].y * ex2_approx(my_rl[w * COLS + col].x - top);
       }
+#pragma unroll
+      for (int w = 0; w < W; ++w) l += my_rl[w * COLS + col].y * ex2_approx(my_rl[w * COLS + col].x - top);
       if (!whole) {
         reinterpret_cast<float4*>(p.part_o + (slot * COLS + col) * D)[c4] = a;
         if (c4 == 0) p.part_rl[slot * COLS + col] = make_float2(top, l);
@@ -621,7 +693,13 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
   }
   if (!ok) {  // its own copies in flight still land in this shared memory
     volatile int no_abort = 0;
-    for (; taken < issued; ++taken) bounded_wait(bars + 8 * (taken % S), (taken / S) & 1u, &no_abort, p.timeout_ns);
+    for (; flying > 0; --flying) {
+      bounded_wait(bars + 8 * stage, phase, &no_abort, p.timeout_ns);
+      if (++stage == S) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
   }
 }
 
@@ -758,12 +836,12 @@ attn_status_t attn_fwd_kv4(const void* q, const void* pool, const int* page_tabl
   p.Hq = Hq;
   p.group = Hq / Hkv;
   p.causal = causal;
-  p.min_units = 16;
+  p.min_units = 8;  // a pair for each of eight warps
   p.scale_log2 = scale * 1.4426950408889634f;
   p.timeout_ns = wait_budget_ns();
   // no more CTAs than the longest possible caches have ranges
   const long long most = ((long long)total_q * p.group / (8 * nt) + num_seqs) * Hkv *
-                         std::max(1LL, ((long long)max_pages * page_size + kKv4Tile - 1) / kKv4Tile);
+                         std::max(1LL, ((long long)max_pages * page_size + kPair * kKv4Tile - 1) / (kPair * kKv4Tile));
   const int ctas = (int)std::max(1LL, std::min<long long>(max_ctas(d, nt), most / p.min_units));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;

@@ -6,7 +6,9 @@
 //   code_c = round((x_c - lo) / s), ties to even (15 at most: s is at least
 //   (1 - 2^-8) (max - lo) / 15);
 // the cache then stands for lo + s * code_c, off by at most s / 2 + 15 * 2^-8 s.
-// A group whose spread is below 15 * 2^-125 is held as its minimum (s = 0). A
+// A group whose spread is below 15 * 2^-125 is held as its minimum (codes of 0;
+// its scale is 2^-13 of the minimum's size, below which no spread of bf16
+// values leads, so that attention can bound its weights by scales alone). A
 // group with a NaN or an infinity is held as NaN (s = NaN, lo = 0).
 //
 // HBM-bound: 5.25 d bytes a token and head each way (bf16 against 5 bits). The
@@ -101,8 +103,9 @@ __device__ __forceinline__ void quantise(const uint4& raw, uint32_t& codes, uint
   if (!(fmaxf(fabsf(lo), fabsf(hi)) < INFINITY) || lo != lo || hi != hi) {
     s_bits = 0x7fc0u;
     lo_bits = 0;
-  } else if (s_bits < 0x0100u) {  // below 2^-125
-    s_bits = 0;
+  } else if (s_bits < 0x0100u) {  // below 2^-125: held as the minimum
+    const uint32_t size = lo_bits & 0x7fffu;
+    s_bits = size >= 0x0100u + (13u << 7) ? size - (13u << 7) : 0u;
   } else {
     const float s = 0.5f * __uint_as_float(s_bits << 16);
     float inv;

@@ -455,8 +455,9 @@ ATTN_API attn_status_t attn_qk_norm_rope_bwd(
  * bf16 minimum lo and scale s and 4-bit codes, standing for lo + s * code with
  *     lo = min_c x_c,  s = bf16((max_c x_c - lo) / 15),
  *     code_c = min(rne((x_c - lo) / s), 15).
- * A group with a spread below 15 * 2^-125 is held as its minimum; a group with
- * a NaN or an infinity is held as NaN.
+ * A group with a spread below 15 * 2^-125 is held as its minimum (s = 2^-13 |lo|
+ * then, 0 if that is below 2^-125); a group with a NaN or an infinity is held as
+ * NaN.
  *   pool        device, uint8 [num_pages][Hkv][page_size / 16][20 d],
  *               16-byte aligned; one page is attn_kv4_page_bytes() bytes. The
  *               record of 16 tokens is laid out in csrc/kv4_format.cuh. Needs
@@ -539,7 +540,8 @@ ATTN_API attn_status_t attn_kv4_copy_pages(void* pool, int num_layers, int num_p
  *            aligned, for one call at a time; needs no initial value
  * Any number of query rows is computed, 8 or 16 (row, head) pairs of a kv head
  * in one pass over its cache; for long chunks attn_kv4_gather and
- * attn_fwd_varlen are faster. |v| up to 2^64. Two launches (attention, merge of
+ * attn_fwd_varlen are faster. |v| up to 2^64; a token's groups whose scale is
+ * below 2^-20 of its largest lose precision. Two launches (attention, merge of
  * what was split); allocates nothing; deterministic.
  */
 ATTN_API size_t attn_fwd_kv4_workspace_size(int Hq, int Hkv, int max_seqlen_q, int d);

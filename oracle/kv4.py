@@ -2,8 +2,8 @@
 attention over what the records stand for, in fp64 (integers for codes).
 
 A token's 32 channels x_c of one kv head (bf16): lo = min x, s = bf16((max x -
-lo) / 15), code = min(rne((x - lo) / s), 15); s below 2^-125 is held as 0, a
-group with a NaN or an infinity as s = NaN, lo = 0.
+lo) / 15), code = min(rne((x - lo) / s), 15); s below 2^-125: codes 0
+and s = 2^-13 |lo| (0 below 2^-125); a group with a NaN or an infinity as s = NaN, lo = 0.
 """
 from __future__ import annotations
 
@@ -32,11 +32,14 @@ def quantise(bits):
     lo, hi = safe.min(-1), safe.max(-1)
     s = (hi - lo) / 15.0
     sb = np.where(s < 2.0 ** -127, 0, round_bf16(np.maximum(s, 2.0 ** -127))).astype(np.uint16)
-    sb = np.where(sb < 0x0100, 0, sb).astype(np.uint16)
+    flat = sb < 0x0100
+    sb = np.where(flat, 0, sb).astype(np.uint16)
     scale = widen_bf16(sb).astype(np.float64)
     q = np.divide(safe - lo[..., None], scale[..., None], out=np.zeros_like(safe), where=scale[..., None] > 0)
     codes = np.minimum(np.rint(q), 15).astype(np.uint8)
     lob = np.take_along_axis(gb, safe.argmin(-1)[..., None], -1)[..., 0]
+    size = (lob & 0x7fff).astype(np.int64) - (13 << 7)
+    sb = np.where(flat, np.where(size >= 0x0100, size, 0), sb)
     sb = np.where(bad, 0x7fc0, sb).astype(np.uint16)
     lob = np.where(bad, 0, lob).astype(np.uint16)
     codes = np.where(bad[..., None], 0, codes)

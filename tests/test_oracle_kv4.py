@@ -65,7 +65,9 @@ def test_quantiser_on_hand():
     assert oracle.widen_bf16(s)[0] == 1.0 and oracle.widen_bf16(lo)[0] == 0.0
     assert codes.tolist() == [0] * 16 + [15] * 8 + [4, 4, 7, 14] * 2     # ties to even
     codes, s, lo = q([-2.5] * 32)                                        # no spread: the minimum
-    assert s[0] == 0 and oracle.widen_bf16(lo)[0] == -2.5 and not codes.any()
+    assert oracle.widen_bf16(s)[0] == 2.5 * 2.0 ** -13 and oracle.widen_bf16(lo)[0] == -2.5 and not codes.any()
+    codes, s, lo = q([0.0] * 32)
+    assert s[0] == 0 and lo[0] == 0 and not codes.any()
     for bad in (float("nan"), float("inf"), -float("inf")):
         codes, s, lo = q([1.0] * 31 + [bad])
         assert s[0] == 0x7fc0 and lo[0] == 0 and not codes.any()
