@@ -36,6 +36,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_internal.h"
 #include "kv4_format.cuh"
@@ -49,6 +50,9 @@ constexpr float kNone = -3.0e38f;     // reference of a row that has seen no key
 constexpr uint32_t kMinScale = 0x1f80u;  // bf16 2^-64: smaller scales count as that, so p stays below 2^79
 constexpr float kRoom = 32768.0f;     // p * s stays below 2^15
 constexpr float kHead = 8.0f;         // log2 of p * s at a new reference: 2^7 of room before the next one
+#ifndef KMU
+#define KMU 8
+#endif
 constexpr int kPair = 2;              // records of a step
 
 struct Kv4Params {
@@ -67,17 +71,20 @@ struct Kv4Params {
   unsigned long long timeout_ns;
 };
 
-template <int D, int NT>
+template <int D, int COLS>
 struct Kv4Cfg {
-  static constexpr int kWarps = (NT == 1 && D <= 128) ? 8 : 4;
-  static constexpr int kCtasPerSm = NT == 2 && D == 64 ? 3 : 2;
+#ifndef KW
+#define KW 4
+#define KC 3
+#endif
+  static constexpr int kWarps = COLS <= 8 && D <= 128 ? KW : 4;
+  static constexpr int kCtasPerSm = D == 64 || (COLS <= 8 && D <= 128) ? KC : 2;
   static constexpr int kStages = 2;
-  static constexpr int kCols = 8 * NT;
   static constexpr int kRecord = kv4_record_bytes(D);
   static constexpr int kStage = kPair * kRecord;
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kJoin = kWarps / 2 * kCols * D * 4;    // fp32 O of half the warps
-  static constexpr int kRl = 2 * kWarps * kCols * 8;          // (reference, sum), two segments
+  static constexpr int kJoin = kWarps / 2 * COLS * D * 4;     // fp32 O of half the warps
+  static constexpr int kRl = 2 * kWarps * COLS * 8;           // (reference, sum), two segments
   static constexpr int kBars = kWarps * kStages * 8;
   static constexpr int kSmemBytes = kRing + kJoin + kRl + kBars + 16;
 };
@@ -87,6 +94,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same onto zeros.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
@@ -225,11 +240,19 @@ __device__ __forceinline__ bool next_segment(const Kv4Params& p, Segment& g) {
   return false;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCtasPerSm)
+template <int D, int COLS>
+__global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>::kCtasPerSm)
     attn_kv4_kernel(const __grid_constant__ Kv4Params p) {
-  using C = Kv4Cfg<D, NT>;
-  constexpr int W = C::kWarps, S = C::kStages, G = D / 32, COLS = C::kCols;
+  using C = Kv4Cfg<D, COLS>;
+  constexpr int W = C::kWarps, S = C::kStages, G = D / 32;
+  static_assert(S == 2 && kPair == 2, "two stages of two records");
+  // At most four rows: an instruction's columns 0 .. 3 take them against record
+  // 0 of a pair, 4 .. 7 the same rows against record 1, so that one set of
+  // scores, weights and scales in the lanes stands for both records.
+  constexpr bool HALF = COLS == 4;
+  constexpr int NT = HALF ? 1 : COLS / 8;  // column tiles
+  constexpr int R = HALF ? 1 : kPair;      // sets of scores of a pair
+  constexpr int Q = HALF ? kPair : 1;      // sets of query operands, by record
   constexpr int MINS = (G + 3) / 4;  // instructions for the minima of a record
   extern __shared__ __align__(128) uint8_t smem[];
   float* const join = reinterpret_cast<float*>(smem + C::kRing);
@@ -286,10 +309,12 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
   };
   pf.t1 = (int)min((long long)pf.s.units, pf.t0 + pf_left);
   int pf_k = 0, pf_count = units(pf);  // next unit of the warp in pf (t0 + warp + W * pf_k), and how many
-  int pf_pages[kPair];    // pages of the records of unit (pf_k / 32) * 32 + lane
+  // of unit (pf_k / 32) * 32 + lane: its records, or null
+  const uint8_t* pf_from[kPair];
   int pf_stage = 0;
   bool pf_more = true;
-  uint32_t bad = 0;       // bits kPair * stage + i: record i of the stage is on no page of the pool
+  uint32_t bad = 0;       // bit i of a stage's two: its record i is on no page of the pool
+  uint32_t pf_bad[kPair]; // of the 32 units
 
   auto issue = [&]() {
     while (pf_k >= pf_count) {
@@ -304,36 +329,33 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
     if ((pf_k & 31) == 0) {
       const int t = kPair * (pf.t0 + warp + W * (pf_k + lane));
 #pragma unroll
-      for (int i = 0; i < kPair; ++i)
-        pf_pages[i] = pf_k + lane < pf_count && (t + i) * kKv4Tile < pf.s.len
-                          ? __ldg(p.c.table + (size_t)pf.b * p.c.max_pages + ((t + i) >> p.c.tiles_log2))
-                          : -1;
-    }
-    const int t = kPair * (pf.t0 + warp + W * pf_k);
-    const uint32_t bar = bars + 8 * pf_stage, to = ring + pf_stage * C::kStage;
-    int page[kPair];
-#pragma unroll
-    for (int i = 0; i < kPair; ++i) page[i] = __shfl_sync(kFull, pf_pages[i], pf_k & 31);
-    const bool two = (t + 1) * kKv4Tile < pf.s.len;
-    const bool ok0 = (unsigned)page[0] < (unsigned)p.c.num_pages, ok1 = two && (unsigned)page[1] < (unsigned)p.c.num_pages;
-    const uint32_t b0 = (ok0 ? 0u : 1u) | (two && !ok1 ? 2u : 0u);
-    bad = (bad & ~(3u << (kPair * pf_stage))) | b0 << (kPair * pf_stage);
-    if (lane == 0) {
-      const int mask = (1 << p.c.tiles_log2) - 1;
-      const uint8_t* const from = p.c.data + kv4_record(p.c, page[0], pf.h, t & mask, D);
-      if (b0 == 0 && two && mask != 0) {  // both in one page: side by side
-        mbar_arrive_expect_tx(bar, C::kStage);
-        bulk_load(to, from, C::kStage, bar);
-      } else {
-        const uint32_t n = (ok0 ? 1u : 0u) + (ok1 ? 1u : 0u);
-        if (n) mbar_arrive_expect_tx(bar, n * C::kRecord);
-        else mbar_arrive(bar);
-        if (ok0) bulk_load(to, from, C::kRecord, bar);
-        if (ok1) bulk_load(to + C::kRecord, p.c.data + kv4_record(p.c, page[1], pf.h, (t + 1) & mask, D), C::kRecord, bar);
-        if (b0) kv4_bad_page(p.status, 0x500);
+      for (int i = 0; i < kPair; ++i) {
+        const bool there = pf_k + lane < pf_count && (t + i) * kKv4Tile < pf.s.len;
+        const int page = there ? __ldg(p.c.table + (size_t)pf.b * p.c.max_pages + ((t + i) >> p.c.tiles_log2)) : -1;
+        const bool ok_ = (unsigned)page < (unsigned)p.c.num_pages;
+        pf_from[i] = ok_ ? p.c.data + kv4_record(p.c, page, pf.h, (t + i) & ((1 << p.c.tiles_log2) - 1), D) : nullptr;
+        pf_bad[i] = __ballot_sync(kFull, there && !ok_);
+        if (there && !ok_) kv4_bad_page(p.status, 0x500);
       }
     }
-    pf_stage = pf_stage + 1 == S ? 0 : pf_stage + 1;
+    const int at = pf_k & 31;
+    const uint32_t b = (pf_bad[0] >> at & 1u) | (pf_bad[1] >> at & 1u) << 1;
+    bad = pf_stage == 0 ? (bad & ~3u) | b : (bad & ~12u) | b << 2;
+    if (lane == at) {  // the unit's own lane
+      const uint32_t bar = bars + 8 * pf_stage, to = ring + pf_stage * C::kStage;
+      const uint8_t *const r0 = pf_from[0], *const r1 = pf_from[1];
+      if (r0 != nullptr && r1 == r0 + C::kRecord) {  // both in one page: side by side
+        mbar_arrive_expect_tx(bar, C::kStage);
+        bulk_load(to, r0, C::kStage, bar);
+      } else {
+        const uint32_t n = (r0 ? 1u : 0u) + (r1 ? 1u : 0u);
+        if (n) mbar_arrive_expect_tx(bar, n * C::kRecord);
+        else mbar_arrive(bar);
+        if (r0) bulk_load(to, r0, C::kRecord, bar);
+        if (r1) bulk_load(to + C::kRecord, r1, C::kRecord, bar);
+      }
+    }
+    pf_stage ^= 1;
     ++pf_k;
     ++flying;
   };
@@ -348,13 +370,13 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
   int turn = 0;  // parity of the segment, for rl
   while (true) {
     // ---- query rows of the segment, as operands
-    uint32_t qf[NT][G][4];
-    uint32_t qmin[NT][MINS][2];  // sums over the groups, for the minima: three bf16 pieces of each
+    uint32_t qf[Q][NT][G][4];
+    uint32_t qmin[Q][NT][MINS][2];  // sums over the groups, for the minima: three bf16 pieces of each
     float fac[NT][2];
     int limit[NT][2];  // last key that the lane's two columns see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = seg.rb * COLS + nt * 8 + g8;
+      const int row = seg.rb * COLS + nt * 8 + g8 % COLS;
       const bool live = row < seg.s.n * p.group;
       const int tok = seg.s.first + row / p.group;
       const uint16_t* const src = p.q + ((size_t)tok * p.Hq + seg.h * p.group + row % p.group) * D + 8 * t4;
@@ -385,10 +407,12 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
           sum += f[i];
         }
         // codes i and i + 4 share a register; 1, 3, 5, 7 stand 4 bits up
-        qf[nt][gr][0] = pack_f16x2(f[0], f[4]);
-        qf[nt][gr][1] = pack_f16x2(f[1] * 0.0625f, f[5] * 0.0625f);
-        qf[nt][gr][2] = pack_f16x2(f[2], f[6]);
-        qf[nt][gr][3] = pack_f16x2(f[3] * 0.0625f, f[7] * 0.0625f);
+        const uint32_t q[4] = {pack_f16x2(f[0], f[4]), pack_f16x2(f[1] * 0.0625f, f[5] * 0.0625f), pack_f16x2(f[2], f[6]),
+                               pack_f16x2(f[3] * 0.0625f, f[7] * 0.0625f)};
+#pragma unroll
+        for (int i = 0; i < Q; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qf[i][nt][gr][e] = HALF && g8 / 4 != i ? 0u : q[e];
         sum += __shfl_xor_sync(kFull, sum, 1);
         sum += __shfl_xor_sync(kFull, sum, 2);
         if (t4 == gr % 4) (gr < 4 ? mine : other) = sum * 5.9604644775390625e-8f;  // 2^-24
@@ -397,15 +421,18 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
       for (int m = 0; m < MINS; ++m) {
         const float s = m ? other : mine;
         const float h = hi16(__float_as_uint(s)), l = hi16(__float_as_uint(s - h));
-        qmin[nt][m][0] = pack_bf16x2(h, l);
-        qmin[nt][m][1] = pack_bf16x2((s - h) - l, 0.0f);
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+          qmin[i][nt][m][0] = HALF && g8 / 4 != i ? 0u : pack_bf16x2(h, l);
+          qmin[i][nt][m][1] = HALF && g8 / 4 != i ? 0u : pack_bf16x2((s - h) - l, 0.0f);
+        }
       }
       // above 0, for the product with a masked score
       const float back = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(24 - k + 127) << 23), 1.17549435e-38f);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {  // the lane's columns 2 t4 + j
         fac[nt][j] = __shfl_sync(kFull, back, 4 * (2 * t4 + j));
-        const int r = seg.rb * COLS + nt * 8 + 2 * t4 + j;
+        const int r = seg.rb * COLS + (nt * 8 + 2 * t4 + j) % COLS;
         limit[nt][j] = p.causal ? seg.s.len - seg.s.n + min(r / p.group, seg.s.n - 1) : seg.s.len - 1;
       }
     }
@@ -433,97 +460,140 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
       if (!ok) break;
       --flying;
       const uint32_t rec = ring + stage * C::kStage;
-      const uint32_t lost = bad >> (kPair * stage) & 3u;
+      const uint32_t lost = bad >> (2 * stage) & 3u;
       const bool edge = key - g8 + kPair * kKv4Tile - 1 > all_see || lost != 0;
 
-      // ---- scores, against the reference
-      float x[kPair][NT][4];
-      uint32_t vs[kPair][G];
+      // halves of a pair of statistics that belong to cached tokens: of keys key + 16 i, + 8
+      auto kept = [&](int i) {
+        const int at = key + kKv4Tile * i, len = lost >> i & 1u ? 0 : seg.s.len;
+        return (at < len ? 0x0000ffffu : 0u) | (at + 8 < len ? 0xffff0000u : 0u);
+      };
+      // ---- scores
+      // the lane's keys in set r: of record r, or of its columns' record
+      const int mine_of = HALF ? t4 >> 1 : 0;
+      float x[R][NT][4];
+      uint32_t vs[R][G];
 #pragma unroll
-      for (int i = 0; i < kPair; ++i) {
-        const uint32_t r = rec + i * C::kRecord;
+      for (int r = 0; r < R; ++r) {
+        const uint32_t own = rec + (HALF ? mine_of : r) * C::kRecord;  // record of the lane's keys
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[i][nt][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) x[r][nt][e] = 0.0f;
         // the minima of key g8 (+ 8) and group t4: once for each of two pieces of the sums
 #pragma unroll
-        for (int m = 0; m < MINS; ++m) {
-          const uint32_t kl = 4 * m + t4 < G ? lds_word(r + 17 * D + (g8 * G + 4 * m + t4) * 4) : 0u;
-          const uint32_t a0 = __byte_perm(kl, kl, 0x1010), a1 = __byte_perm(kl, kl, 0x3232);
+        for (int i = 0; i < Q; ++i) {
+          const uint32_t at = rec + (HALF ? i : r) * C::kRecord;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_bf16_full(x[i][nt], a0, a1, a0, a1, qmin[nt][m][0], qmin[nt][m][1]);
-        }
-        uint32_t ks[G];
-        lds_words<G>(ks, r + 16 * D + g8 * G * 4);
+          for (int m = 0; m < MINS; ++m) {
+            uint32_t kl = 4 * m + t4 < G ? lds_word(at + 17 * D + (g8 * G + 4 * m + t4) * 4) : 0u;
+            if (HALF && edge) kl &= kept(i);  // a NaN would reach the other record's columns
+            const uint32_t a0 = __byte_perm(kl, kl, 0x1010), a1 = __byte_perm(kl, kl, 0x3232);
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-          uint32_t w0, w1;
-          lds_pair(w0, w1, r + gr * 256 + lane * 8);
-          const float s0 = lo16(ks[gr]), s1 = hi16(ks[gr]);
-          const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma_f16(acc, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, qf[nt][gr][0],
-                    qf[nt][gr][1]);
-            mma_f16(acc, v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u, qf[nt][gr][2],
-                    qf[nt][gr][3]);
-            x[i][nt][0] = fmaf(s0, acc[0], x[i][nt][0]);
-            x[i][nt][1] = fmaf(s0, acc[1], x[i][nt][1]);
-            x[i][nt][2] = fmaf(s1, acc[2], x[i][nt][2]);
-            x[i][nt][3] = fmaf(s1, acc[3], x[i][nt][3]);
+            for (int nt = 0; nt < NT; ++nt) mma_bf16_full(x[r][nt], a0, a1, a0, a1, qmin[i][nt][m][0], qmin[i][nt][m][1]);
           }
         }
-        lds_words<G>(vs[i], r + 18 * D + g8 * G * 4);
+        uint32_t ks[G];
+        lds_words<G>(ks, own + 16 * D + g8 * G * 4);
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+          const float s0 = lo16(ks[gr]), s1 = hi16(ks[gr]);
+          float acc[NT][4];
+#pragma unroll
+          for (int i = 0; i < Q; ++i) {
+            uint32_t w0, w1;
+            lds_pair(w0, w1, rec + (HALF ? i : r) * C::kRecord + gr * 256 + lane * 8);
+            const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (i == 0)
+                mma_f16_first(acc[nt], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u,
+                              qf[i][nt][gr][0], qf[i][nt][gr][1]);
+              else
+                mma_f16(acc[nt], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u,
+                        qf[i][nt][gr][0], qf[i][nt][gr][1]);
+              mma_f16(acc[nt], v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u, qf[i][nt][gr][2],
+                      qf[i][nt][gr][3]);
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            x[r][nt][0] = fmaf(s0, acc[nt][0], x[r][nt][0]);
+            x[r][nt][1] = fmaf(s0, acc[nt][1], x[r][nt][1]);
+            x[r][nt][2] = fmaf(s1, acc[nt][2], x[r][nt][2]);
+            x[r][nt][3] = fmaf(s1, acc[nt][3], x[r][nt][3]);
+          }
+        }
+        lds_words<G>(vs[r], own + 18 * D + g8 * G * 4);
       }
+      uint32_t vm[kPair][2];
+#pragma unroll
+      for (int i = 0; i < kPair; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          vm[i][e] = g8 < G ? lds_word(rec + i * C::kRecord + 19 * D + g8 * 32 + 16 * e + t4 * 4) : 0u;
+      bool hidden = false;  // NaN scales beside keys that some row does not see
       if (edge) {
-        // keys behind the cached ones hold anything: no scale of theirs counts;
-        // keys that a row does not see get -inf
+        // keys behind the cached ones hold anything: no scale or minimum of
+        // theirs counts; keys that a row does not see get -inf
 #pragma unroll
-        for (int i = 0; i < kPair; ++i) {
-          const int at = key + kKv4Tile * i, len = lost >> i & 1u ? 0 : seg.s.len;
-          const uint32_t keep = (at < len ? 0x0000ffffu : 0u) | (at + 8 < len ? 0xffff0000u : 0u);
+        for (int r = 0; r < R; ++r) {
+          const int i = HALF ? mine_of : r;
+          const int at = key + kKv4Tile * i;
+          const uint32_t keep = kept(i);
+          uint32_t top = 0;
 #pragma unroll
-          for (int gr = 0; gr < G; ++gr) vs[i][gr] &= keep;
+          for (int gr = 0; gr < G; ++gr) {
+            vs[r][gr] &= keep;
+            top = __vmaxu2(top, vs[r][gr]);
+          }
+          hidden |= (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (at + (e & 2) * 4 > limit[nt][e & 1] || !(keep >> (e & 2) * 8 & 1u)) x[i][nt][e] = -INFINITY;
+              if (at + (e & 2) * 4 > limit[nt][e & 1] || !(keep >> (e & 2) * 8 & 1u)) x[r][nt][e] = -INFINITY;
         }
+#pragma unroll
+        for (int i = 0; i < kPair; ++i) {
+          const int pair = key - g8 + kKv4Tile * i + 2 * t4, len = lost >> i & 1u ? 0 : seg.s.len;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            vm[i][e] &= (pair + 8 * e < len ? 0x0000ffffu : 0u) | (pair + 8 * e + 1 < len ? 0xffff0000u : 0u);
+        }
+        hidden = __any_sync(kFull, hidden);
       }
       // ---- weights; a new reference where p * s would pass 2^15. The bound of s
       // is each key's own, over its groups
-      float pr[kPair][NT][4];
+      float pr[R][NT][4];
       bool over = false;
 #pragma unroll
-      for (int i = 0; i < kPair; ++i) {
+      for (int r = 0; r < R; ++r) {
         uint32_t top = kMinScale | kMinScale << 16;
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) top = __vmaxu2(top, vs[i][gr]);
+        for (int gr = 0; gr < G; ++gr) top = __vmaxu2(top, vs[r][gr]);
         const float s0 = lo16(top), s1 = hi16(top);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) pr[i][nt][e] = ex2_approx(fmaf(x[i][nt][e], fac[nt][e & 1], -ref[nt][e & 1]));
-          const float m0 = fmaxf(pr[i][nt][0], pr[i][nt][1]) * s0, m1 = fmaxf(pr[i][nt][2], pr[i][nt][3]) * s1;
+          for (int e = 0; e < 4; ++e) pr[r][nt][e] = ex2_approx(fmaf(x[r][nt][e], fac[nt][e & 1], -ref[nt][e & 1]));
+          const float m0 = fmaxf(pr[r][nt][0], pr[r][nt][1]) * s0, m1 = fmaxf(pr[r][nt][2], pr[r][nt][3]) * s1;
           over |= !(m0 < kRoom) || !(m1 < kRoom);  // NaN scales too
         }
       }
       if (__any_sync(kFull, over)) {
-        float bound[kPair][2];  // log2 of the keys' scales, NaN ones left out
+        float bound[R][2];  // log2 of the keys' scales, NaN ones left out
 #pragma unroll
-        for (int i = 0; i < kPair; ++i) {
+        for (int r = 0; r < R; ++r) {
           uint32_t t0 = kMinScale, t1 = kMinScale;
 #pragma unroll
           for (int gr = 0; gr < G; ++gr) {
-            const uint32_t a = vs[i][gr] & 0xffffu, b = vs[i][gr] >> 16;
+            const uint32_t a = vs[r][gr] & 0xffffu, b = vs[r][gr] >> 16;
             t0 = max(t0, a < 0x7f80u ? a : 0u);
             t1 = max(t1, b < 0x7f80u ? b : 0u);
           }
-          bound[i][0] = (float)((int)(t0 >> 7) - 126);
-          bound[i][1] = (float)((int)(t1 >> 7) - 126);
+          bound[r][0] = (float)((int)(t0 >> 7) - 126);
+          bound[r][1] = (float)((int)(t1 >> 7) - 126);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -531,8 +601,9 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
           for (int j = 0; j < 2; ++j) {
             float m = kNone;
 #pragma unroll
-            for (int i = 0; i < kPair; ++i)
-              m = fmaxf(m, fmaxf(fmaf(x[i][nt][j], fac[nt][j], bound[i][0]), fmaf(x[i][nt][2 + j], fac[nt][j], bound[i][1])));
+            for (int r = 0; r < R; ++r)
+              m = fmaxf(m, fmaxf(fmaf(x[r][nt][j], fac[nt][j], bound[r][0]), fmaf(x[r][nt][2 + j], fac[nt][j], bound[r][1])));
+            if (HALF) m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));  // one reference for a row's two columns
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
             const float next = fmaxf(ref[nt][j], m - kHead);
@@ -546,67 +617,79 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
             }
             omin[nt][j] *= f;
 #pragma unroll
-            for (int i = 0; i < kPair; ++i) {
-              pr[i][nt][j] = ex2_approx(fmaf(x[i][nt][j], fac[nt][j], -next));
-              pr[i][nt][2 + j] = ex2_approx(fmaf(x[i][nt][2 + j], fac[nt][j], -next));
+            for (int r = 0; r < R; ++r) {
+              pr[r][nt][j] = ex2_approx(fmaf(x[r][nt][j], fac[nt][j], -next));
+              pr[r][nt][2 + j] = ex2_approx(fmaf(x[r][nt][2 + j], fac[nt][j], -next));
             }
           }
       }
       // ---- O^T += V^T P^T
+      // with HALF an operand's columns of the other record are cleared
+      const uint32_t low = g8 < 4 ? 0xffffffffu : 0u;
+      auto of = [&](uint32_t v, int i) { return !HALF ? v : i ? v & ~low : v & low; };
 #pragma unroll
-      for (int i = 0; i < kPair; ++i) {
-        const uint32_t r = rec + i * C::kRecord;
-        uint32_t vm[2];
-        vm[0] = g8 < G ? lds_word(r + 19 * D + g8 * 32 + t4 * 4) : 0u;
-        vm[1] = g8 < G ? lds_word(r + 19 * D + g8 * 32 + 16 + t4 * 4) : 0u;
-        if (edge) {
-          const int pair = key - g8 + kKv4Tile * i + 2 * t4, len = lost >> i & 1u ? 0 : seg.s.len;
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            vm[e] &= (pair + 8 * e < len ? 0x0000ffffu : 0u) | (pair + 8 * e + 1 < len ? 0xffff0000u : 0u);
-        }
+      for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float(&pe)[4] = pr[i][nt];
+          const float(&pe)[4] = pr[r][nt];
           sum[nt][0] += pe[0] + pe[2];
           sum[nt][1] += pe[1] + pe[3];
           // the minimum's weights in two bf16 steps (16 bits): the minimum and
           // the codes' part cancel, so a single one would show in the result
-          const uint32_t h0 = __byte_perm(__float_as_uint(pe[0]), __float_as_uint(pe[1]), 0x7632);
-          const uint32_t h1 = __byte_perm(__float_as_uint(pe[2]), __float_as_uint(pe[3]), 0x7632);
-          const uint32_t l0 = pack_bf16x2(pe[0] - lo16(h0), pe[1] - hi16(h0));
-          const uint32_t l1 = pack_bf16x2(pe[2] - lo16(h1), pe[3] - hi16(h1));
-          mma_bf16(omin[nt], vm[0], vm[1], transpose8(h0), transpose8(h1));
-          mma_bf16(omin[nt], vm[0], vm[1], transpose8(l0), transpose8(l1));
-        }
+          uint32_t h0 = __byte_perm(__float_as_uint(pe[0]), __float_as_uint(pe[1]), 0x7632);
+          uint32_t h1 = __byte_perm(__float_as_uint(pe[2]), __float_as_uint(pe[3]), 0x7632);
+          const uint32_t l0 = transpose8(pack_bf16x2(pe[0] - lo16(h0), pe[1] - hi16(h0)));
+          const uint32_t l1 = transpose8(pack_bf16x2(pe[2] - lo16(h1), pe[3] - hi16(h1)));
+          h0 = transpose8(h0);
+          h1 = transpose8(h1);
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-          uint32_t a, b;
-          lds_pair(a, b, r + 8 * D + gr * 256 + lane * 8);
-          const float s0 = lo16(vs[i][gr]), s1 = hi16(vs[i][gr]);
-          const uint32_t a8 = a >> 8, b8 = b >> 8;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const float(&pe)[4] = pr[i][nt];
-            float w[4] = {pe[0] * s0, pe[1] * s0, pe[2] * s1, pe[3] * s1};
-            if (edge) {  // a NaN group reaches only the rows that see its key
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (x[i][nt][e] == -INFINITY) w[e] = 0.0f;
-            }
-            const uint32_t p0 = transpose8(pack_f16x2(w[0], w[1])), p1 = transpose8(pack_f16x2(w[2], w[3]));
-            mma_f16(o[nt][2 * gr], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u, p0, p1);
-            mma_f16(o[nt][2 * gr + 1], a8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x000f000fu, b8 & 0x00f000f0u, p0, p1);
+          for (int i = 0; i < Q; ++i) {
+            const uint32_t(&v)[2] = vm[HALF ? i : r];
+            mma_bf16(omin[nt], v[0], v[1], of(h0, i), of(h1, i));
+            mma_bf16(omin[nt], v[0], v[1], of(l0, i), of(l1, i));
           }
         }
-      }
+      auto values = [&](auto masked) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr) {
+            const float s0 = lo16(vs[r][gr]), s1 = hi16(vs[r][gr]);
+            uint32_t p0[NT], p1[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float(&pe)[4] = pr[r][nt];
+              float w[4] = {pe[0] * s0, pe[1] * s0, pe[2] * s1, pe[3] * s1};
+              if (decltype(masked)::value) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (x[r][nt][e] == -INFINITY) w[e] = 0.0f;
+              }
+              p0[nt] = transpose8(pack_f16x2(w[0], w[1]));
+              p1[nt] = transpose8(pack_f16x2(w[2], w[3]));
+            }
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+              uint32_t a, b;
+              lds_pair(a, b, rec + (HALF ? i : r) * C::kRecord + 8 * D + gr * 256 + lane * 8);
+              const uint32_t a8 = a >> 8, b8 = b >> 8;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t q0 = of(p0[nt], i), q1 = of(p1[nt], i);
+                mma_f16(o[nt][2 * gr], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u, q0, q1);
+                mma_f16(o[nt][2 * gr + 1], a8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x000f000fu, b8 & 0x00f000f0u, q0, q1);
+              }
+            }
+          }
+      };
+      // a NaN group reaches only the rows that see its key
+      if (!hidden) values(std::false_type());
+      else values(std::true_type());
       // ---- the stage is free
       __syncwarp();
       issue();
-      if (++stage == S) {
-        stage = 0;
-        phase ^= 1u;
-      }
+      phase ^= (uint32_t)stage;
+      stage ^= 1;
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
@@ -614,6 +697,19 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
     }
 
     // ---- join the warps
+    if (HALF) {  // first a row's two columns: their reference is one
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        sum[0][j] += __shfl_xor_sync(kFull, sum[0][j], 2);
+        omin[0][j] += __shfl_xor_sync(kFull, omin[0][j], 2);
+#pragma unroll
+        for (int m = 0; m < 2 * G; ++m) {
+          o[0][m][j] += __shfl_xor_sync(kFull, o[0][m][j], 2);
+          o[0][m][2 + j] += __shfl_xor_sync(kFull, o[0][m][2 + j], 2);
+        }
+      }
+    }
+    const bool column = !HALF || t4 < 2;  // the lane's columns are rows
     float2* const my_rl = rl + turn * W * COLS;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -621,7 +717,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) sum[nt][j] += __shfl_xor_sync(kFull, sum[nt][j], d);
-        if (g8 == 0) my_rl[warp * COLS + nt * 8 + 2 * t4 + j] = make_float2(ref[nt][j], sum[nt][j]);
+        if (g8 == 0 && column) my_rl[warp * COLS + nt * 8 + 2 * t4 + j] = make_float2(ref[nt][j], sum[nt][j]);
       }
     __syncthreads();
     // O of the upper half of the warps, then the lower half's added to it
@@ -632,7 +728,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int col = nt * 8 + 2 * t4 + j;
+            const int col = (nt * 8 + 2 * t4 + j) % COLS;
             float top = my_rl[col].x;
 #pragma unroll
             for (int w = 1; w < W; ++w) top = fmaxf(top, my_rl[w * COLS + col].x);
@@ -645,11 +741,11 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
               float4 v = make_float4(fmaf(f0, o[nt][2 * gr][j], lo), fmaf(f1, o[nt][2 * gr][2 + j], lo),
                                      fmaf(f0, o[nt][2 * gr + 1][j], lo), fmaf(f1, o[nt][2 * gr + 1][2 + j], lo));
               float4* const at = reinterpret_cast<float4*>(to + 32 * gr);
-              if (half == 0) {
+              if (half == 0 && column) {
                 const float4 u = *at;
                 v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
               }
-              *at = v;
+              if (column) *at = v;
             }
           }
       }
@@ -695,56 +791,58 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::kWarps * 32, Kv4Cfg<D, NT>::kCt
     volatile int no_abort = 0;
     for (; flying > 0; --flying) {
       bounded_wait(bars + 8 * stage, phase, &no_abort, p.timeout_ns);
-      if (++stage == S) {
-        stage = 0;
-        phase ^= 1u;
-      }
+      phase ^= (uint32_t)stage;
+      stage ^= 1;
     }
   }
 }
 
 // Joins the partial results of the row block that border `blockIdx.x + 1` cuts
-// first, one column (query row) a block: O = sum_c 2^(R_c - R) O_c / sum_c 2^(R_c - R) l_c.
-constexpr int kMergeSlices = 8;
-template <int D>
-__global__ void __launch_bounds__(D / 4 * kMergeSlices) attn_kv4_merge_kernel(const __grid_constant__ Kv4Params p, int cols) {
-  constexpr int T = D / 4;
-  __shared__ float4 acc[kMergeSlices][T];
-  __shared__ float tops[kMergeSlices], sums[kMergeSlices];
+// first: O = sum_c 2^(R_c - R) O_c / sum_c 2^(R_c - R) l_c. A thread has four
+// channels of a column (query row) and a slice of the parts.
+constexpr int kMergeThreads = 1024;
+template <int D, int COLS>
+__global__ void __launch_bounds__(kMergeThreads) attn_kv4_merge_kernel(const __grid_constant__ Kv4Params p) {
+  constexpr int T = D / 4, COLUMN = COLS * T, SLICES = kMergeThreads / COLUMN;
+  __shared__ float4 acc[SLICES][COLUMN];
+  __shared__ float tops[SLICES][COLS], sums[SLICES][COLS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 a = p.split[2 * (blockIdx.x + 1)], z = p.split[2 * (blockIdx.x + 1) + 1];
   if (a.x == 0) return;
-  const int col = blockIdx.y, r = z.x * cols + col;
-  if (r >= z.z * p.group) return;
-  const int c4 = threadIdx.x % T, slice = threadIdx.x / T;
+  const int slice = threadIdx.x / COLUMN, at = threadIdx.x % COLUMN, col = at / T, c4 = at % T;
+  const int r = z.x * COLS + col;
+  const bool live = slice < SLICES && r < z.z * p.group;
   // parts: the last slot of CTA a.y, then the first slots of a.y + 1 .. a.z
   float top = kNone, l = 0.0f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = a.y + slice; c <= a.z; c += kMergeSlices) {
-    const size_t at = (size_t)(2 * c + (c == a.y ? 1 : 0)) * cols + col;
-    const float2 rl = p.part_rl[at];
-    const float4 x = reinterpret_cast<const float4*>(p.part_o + at * D)[c4];
-    const float next = fmaxf(top, rl.x), f = ex2_approx(top - next), g = ex2_approx(rl.x - next);
-    top = next;
-    l = l * f + rl.y * g;
-    v = make_float4(v.x * f + x.x * g, v.y * f + x.y * g, v.z * f + x.z * g, v.w * f + x.w * g);
-  }
-  acc[slice][c4] = v;
-  if (c4 == 0) {
-    tops[slice] = top;
-    sums[slice] = l;
+  if (live) {
+#pragma unroll 4
+    for (int c = a.y + slice; c <= a.z; c += SLICES) {
+      const size_t part = (size_t)(2 * c + (c == a.y ? 1 : 0)) * COLS + col;
+      const float2 rl = p.part_rl[part];
+      const float4 x = reinterpret_cast<const float4*>(p.part_o + part * D)[c4];
+      const float next = fmaxf(top, rl.x), f = ex2_approx(top - next), g = ex2_approx(rl.x - next);
+      top = next;
+      l = l * f + rl.y * g;
+      v = make_float4(v.x * f + x.x * g, v.y * f + x.y * g, v.z * f + x.z * g, v.w * f + x.w * g);
+    }
+    acc[slice][at] = v;
+    if (c4 == 0) {
+      tops[slice][col] = top;
+      sums[slice][col] = l;
+    }
   }
   __syncthreads();
-  if (slice != 0) return;
+  if (slice != 0 || !live) return;
 #pragma unroll
-  for (int i = 1; i < kMergeSlices; ++i) top = fmaxf(top, tops[i]);
+  for (int i = 1; i < SLICES; ++i) top = fmaxf(top, tops[i][col]);
   l = 0.0f;
   v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < kMergeSlices; ++i) {
-    const float f = ex2_approx(tops[i] - top);
-    const float4 x = acc[i][c4];
-    l += f * sums[i];
+  for (int i = 0; i < SLICES; ++i) {
+    const float f = ex2_approx(tops[i][col] - top);
+    const float4 x = acc[i][at];
+    l += f * sums[i][col];
     v = make_float4(v.x + f * x.x, v.y + f * x.y, v.z + f * x.z, v.w + f * x.w);
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -754,43 +852,52 @@ __global__ void __launch_bounds__(D / 4 * kMergeSlices) attn_kv4_merge_kernel(co
   if (c4 == 0) p.lse[(size_t)head * p.c.total + tok] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
 }
 
-// Rows of a kv head in one pass over its records: 8 columns, or 16 where a
-// sequence has more rows (at d = 256 their accumulators do not fit).
-int row_tiles(int d, long long rows) { return d <= 128 && rows > 8 ? 2 : 1; }
+// Rows of a kv head in one pass over its records: 4, 8, or 16 columns by the
+// rows that a sequence has (at d = 256 the accumulators of 16 do not fit).
+int row_cols(int d, long long rows) { return rows <= 4 ? 4 : rows <= 8 || d > 128 ? 8 : 16; }
 
 // Most CTAs of a launch: those that are resident at once.
-int max_ctas(int d, int nt) { return 148 * (nt == 2 && d == 64 ? 3 : 2); }
+int max_ctas(int d, int cols) { return 148 * (d == 64 || (cols <= 8 && d <= 128) ? KC : 2); }
 
 struct Kv4Workspace {
   size_t rl, split, total;
 };
-Kv4Workspace workspace(int d, int nt) {
-  const size_t slots = 2 * (size_t)max_ctas(d, nt) * 8 * nt;
+Kv4Workspace workspace(int d, int cols) {
+  const size_t slots = 2 * (size_t)max_ctas(d, cols) * cols;
   Kv4Workspace w;
   w.rl = slots * d * 4;
   w.split = w.rl + slots * sizeof(float2);
-  w.total = (w.split + 2 * (size_t)max_ctas(d, nt) * sizeof(int4) + 255) / 256 * 256;
+  w.total = (w.split + 2 * (size_t)max_ctas(d, cols) * sizeof(int4) + 255) / 256 * 256;
   return w;
 }
 
-template <int D, int NT>
+template <int D, int COLS>
 cudaError_t launch_kv4(const Kv4Params& p, int ctas, cudaStream_t stream) {
-  using C = Kv4Cfg<D, NT>;
-  cudaError_t e = max_dynamic_smem_once<attn_kv4_kernel<D, NT>>(C::kSmemBytes);
+  using C = Kv4Cfg<D, COLS>;
+  cudaError_t e = max_dynamic_smem_once<attn_kv4_kernel<D, COLS>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  attn_kv4_kernel<D, NT><<<ctas, C::kWarps * 32, C::kSmemBytes, stream>>>(p);
+  attn_kv4_kernel<D, COLS><<<ctas, C::kWarps * 32, C::kSmemBytes, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas - 1, C::kCols);
-  cfg.blockDim = dim3(D / 4 * kMergeSlices);
+  cfg.gridDim = dim3(ctas - 1);
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_kv4_merge_kernel<D>, p, C::kCols);
+  return cudaLaunchKernelEx(&cfg, attn_kv4_merge_kernel<D, COLS>, p);
+}
+
+template <int D>
+cudaError_t launch_cols(const Kv4Params& p, int cols, int ctas, cudaStream_t stream) {
+  if (cols == 4) return launch_kv4<D, 4>(p, ctas, stream);
+  if constexpr (D <= 128) {
+    if (cols == 16) return launch_kv4<D, 16>(p, ctas, stream);
+  }
+  return launch_kv4<D, 8>(p, ctas, stream);
 }
 
 }  // namespace
@@ -802,7 +909,7 @@ extern "C" {
 
 size_t attn_fwd_kv4_workspace_size(int Hq, int Hkv, int max_seqlen_q, int d) {
   if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || max_seqlen_q <= 0 || (d != 64 && d != 96 && d != 128 && d != 256)) return 0;
-  return workspace(d, row_tiles(d, (long long)max_seqlen_q * (Hq / Hkv))).total;
+  return workspace(d, row_cols(d, (long long)max_seqlen_q * (Hq / Hkv))).total;
 }
 
 attn_status_t attn_fwd_kv4(const void* q, const void* pool, const int* page_table, const int* seq_lens,
@@ -820,8 +927,8 @@ attn_status_t attn_fwd_kv4(const void* q, const void* pool, const int* page_tabl
   if ((long long)total_q * (Hq / Hkv) > 0x7fffff00LL) return ATTN_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(lse)) & 15u)
     return ATTN_ERR_ALIGNMENT;
-  const int nt = row_tiles(d, (long long)max_seqlen_q * (Hq / Hkv));
-  const Kv4Workspace w = workspace(d, nt);
+  const int cols = row_cols(d, (long long)max_seqlen_q * (Hq / Hkv));
+  const Kv4Workspace w = workspace(d, cols);
   if (!workspace_ptr || (reinterpret_cast<uintptr_t>(workspace_ptr) & 15u) || workspace_bytes < w.total)
     return ATTN_ERR_WORKSPACE;
   p.status = device_status_word();
@@ -836,20 +943,20 @@ attn_status_t attn_fwd_kv4(const void* q, const void* pool, const int* page_tabl
   p.Hq = Hq;
   p.group = Hq / Hkv;
   p.causal = causal;
-  p.min_units = 8;  // a pair for each of eight warps
+  p.min_units = KMU;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.timeout_ns = wait_budget_ns();
   // no more CTAs than the longest possible caches have ranges
-  const long long most = ((long long)total_q * p.group / (8 * nt) + num_seqs) * Hkv *
+  const long long most = ((long long)total_q * p.group / cols + num_seqs) * Hkv *
                          std::max(1LL, ((long long)max_pages * page_size + kPair * kKv4Tile - 1) / (kPair * kKv4Tile));
-  const int ctas = (int)std::max(1LL, std::min<long long>(max_ctas(d, nt), most / p.min_units));
+  const int ctas = (int)std::max(1LL, std::min<long long>(max_ctas(d, cols), most / p.min_units));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   switch (d) {
-    case 64: e = nt == 1 ? launch_kv4<64, 1>(p, ctas, st) : launch_kv4<64, 2>(p, ctas, st); break;
-    case 96: e = nt == 1 ? launch_kv4<96, 1>(p, ctas, st) : launch_kv4<96, 2>(p, ctas, st); break;
-    case 128: e = nt == 1 ? launch_kv4<128, 1>(p, ctas, st) : launch_kv4<128, 2>(p, ctas, st); break;
-    default: e = launch_kv4<256, 1>(p, ctas, st); break;
+    case 64: e = launch_cols<64>(p, cols, ctas, st); break;
+    case 96: e = launch_cols<96>(p, cols, ctas, st); break;
+    case 128: e = launch_cols<128>(p, cols, ctas, st); break;
+    default: e = launch_cols<256>(p, cols, ctas, st); break;
   }
   return cuda_error_status(e);
 }
