@@ -85,8 +85,12 @@ struct Kv4Cfg {
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kJoin = kWarps / 2 * COLS * D * 4;     // fp32 O of half the warps
   static constexpr int kRl = 2 * kWarps * COLS * 8;           // (reference, sum), two segments
+  // query operands of the segment: [record sets * column tiles][groups][lane] of
+  // 16 bytes, of 8 bytes for the minima, and a factor a column
+  static constexpr int kTiles = COLS == 4 ? kPair : COLS / 8, kMins = (D / 32 + 3) / 4;
+  static constexpr int kQ = kTiles * (D / 32) * 512, kQm = kTiles * kMins * 256;
   static constexpr int kBars = kWarps * kStages * 8;
-  static constexpr int kSmemBytes = kRing + kJoin + kRl + kBars + 16;
+  static constexpr int kSmemBytes = kRing + kJoin + kRl + kQ + kQm + COLS * 4 + kBars + 16;
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -257,10 +261,14 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
   extern __shared__ __align__(128) uint8_t smem[];
   float* const join = reinterpret_cast<float*>(smem + C::kRing);
   float2* const rl = reinterpret_cast<float2*>(smem + C::kRing + C::kJoin);
-  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + C::kRing + C::kJoin + C::kRl + C::kBars);
+  uint8_t* const q_smem = smem + C::kRing + C::kJoin + C::kRl;
+  float* const fac_smem = reinterpret_cast<float*>(q_smem + C::kQ + C::kQm);
+  uint8_t* const bar_smem = q_smem + C::kQ + C::kQm + COLS * 4;
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(bar_smem + C::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
   const uint32_t ring = smem_addr(smem) + warp * S * C::kStage;
-  const uint32_t bars = smem_addr(smem + C::kRing + C::kJoin + C::kRl) + warp * S * 8;
+  const uint32_t bars = smem_addr(bar_smem) + warp * S * 8;
+  const uint32_t qs = smem_addr(q_smem) + lane * 16, qms = smem_addr(q_smem + C::kQ) + lane * 8;
 
   if (lane == 0) {
 #pragma unroll
@@ -309,12 +317,14 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
   };
   pf.t1 = (int)min((long long)pf.s.units, pf.t0 + pf_left);
   int pf_k = 0, pf_count = units(pf);  // next unit of the warp in pf (t0 + warp + W * pf_k), and how many
-  // of unit (pf_k / 32) * 32 + lane: its records, or null
-  const uint8_t* pf_from[kPair];
+  // of unit (pf_k / 32) * 32 + lane: its records, and the bytes to copy from
+  // each (both from the first if they lie side by side)
+  const uint8_t *pf_from0 = nullptr, *pf_from1 = nullptr;
+  uint32_t pf_bytes0 = 0, pf_bytes1 = 0;
   int pf_stage = 0;
   bool pf_more = true;
-  uint32_t bad = 0;       // bit i of a stage's two: its record i is on no page of the pool
-  uint32_t pf_bad[kPair]; // of the 32 units
+  uint32_t pf_bad0 = 0, pf_bad1 = 0;  // of the 32 units: a record on no page of the pool
+  uint32_t bad = 0;                   // the same, two bits each, of the stages on their way
 
   auto issue = [&]() {
     while (pf_k >= pf_count) {
@@ -328,33 +338,28 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
     }
     if ((pf_k & 31) == 0) {
       const int t = kPair * (pf.t0 + warp + W * (pf_k + lane));
-#pragma unroll
-      for (int i = 0; i < kPair; ++i) {
-        const bool there = pf_k + lane < pf_count && (t + i) * kKv4Tile < pf.s.len;
-        const int page = there ? __ldg(p.c.table + (size_t)pf.b * p.c.max_pages + ((t + i) >> p.c.tiles_log2)) : -1;
+      auto record = [&](int t_, uint32_t& bad_) {
+        const bool there = pf_k + lane < pf_count && t_ * kKv4Tile < pf.s.len;
+        const int page = there ? __ldg(p.c.table + (size_t)pf.b * p.c.max_pages + (t_ >> p.c.tiles_log2)) : -1;
         const bool ok_ = (unsigned)page < (unsigned)p.c.num_pages;
-        pf_from[i] = ok_ ? p.c.data + kv4_record(p.c, page, pf.h, (t + i) & ((1 << p.c.tiles_log2) - 1), D) : nullptr;
-        pf_bad[i] = __ballot_sync(kFull, there && !ok_);
+        bad_ = __ballot_sync(kFull, there && !ok_);
         if (there && !ok_) kv4_bad_page(p.status, 0x500);
-      }
+        return ok_ ? p.c.data + kv4_record(p.c, page, pf.h, t_ & ((1 << p.c.tiles_log2) - 1), D) : nullptr;
+      };
+      pf_from0 = record(t, pf_bad0);
+      pf_from1 = record(t + 1, pf_bad1);
+      const bool side = pf_from0 != nullptr && pf_from1 == pf_from0 + C::kRecord;
+      pf_bytes0 = side ? C::kStage : pf_from0 ? C::kRecord : 0;
+      pf_bytes1 = !side && pf_from1 ? C::kRecord : 0;
     }
     const int at = pf_k & 31;
-    const uint32_t b = (pf_bad[0] >> at & 1u) | (pf_bad[1] >> at & 1u) << 1;
-    bad = pf_stage == 0 ? (bad & ~3u) | b : (bad & ~12u) | b << 2;
     if (lane == at) {  // the unit's own lane
       const uint32_t bar = bars + 8 * pf_stage, to = ring + pf_stage * C::kStage;
-      const uint8_t *const r0 = pf_from[0], *const r1 = pf_from[1];
-      if (r0 != nullptr && r1 == r0 + C::kRecord) {  // both in one page: side by side
-        mbar_arrive_expect_tx(bar, C::kStage);
-        bulk_load(to, r0, C::kStage, bar);
-      } else {
-        const uint32_t n = (r0 ? 1u : 0u) + (r1 ? 1u : 0u);
-        if (n) mbar_arrive_expect_tx(bar, n * C::kRecord);
-        else mbar_arrive(bar);
-        if (r0) bulk_load(to, r0, C::kRecord, bar);
-        if (r1) bulk_load(to + C::kRecord, r1, C::kRecord, bar);
-      }
+      mbar_arrive_expect_tx(bar, pf_bytes0 + pf_bytes1);
+      if (pf_bytes0) bulk_load(to, pf_from0, pf_bytes0, bar);
+      if (pf_bytes1) bulk_load(to + C::kRecord, pf_from1, pf_bytes1, bar);
     }
+    if (pf_bad0 | pf_bad1) bad |= ((pf_bad0 >> at & 1u) | (pf_bad1 >> at & 1u) << 1) << (2 * flying);
     pf_stage ^= 1;
     ++pf_k;
     ++flying;
@@ -369,13 +374,10 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
   uint32_t phase = 0;
   int turn = 0;  // parity of the segment, for rl
   while (true) {
-    // ---- query rows of the segment, as operands
-    uint32_t qf[Q][NT][G][4];
-    uint32_t qmin[Q][NT][MINS][2];  // sums over the groups, for the minima: three bf16 pieces of each
+    // ---- query rows of the segment, as operands: a column tile by each warp
     float fac[NT][2];
     int limit[NT][2];  // last key that the lane's two columns see
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = warp; nt < NT; nt += W) {
       const int row = seg.rb * COLS + nt * 8 + g8 % COLS;
       const bool live = row < seg.s.n * p.group;
       const int tok = seg.s.first + row / p.group;
@@ -385,11 +387,10 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
 #pragma unroll
       for (int gr = 0; gr < G; ++gr) {
         raw[gr] = live ? __ldg(reinterpret_cast<const uint4*>(src + 32 * gr)) : make_uint4(0, 0, 0, 0);
-        top = max(max(top, max(raw[gr].x & 0x7fffu, (raw[gr].x >> 16) & 0x7fffu)),
-                  max(raw[gr].y & 0x7fffu, (raw[gr].y >> 16) & 0x7fffu));
-        top = max(max(top, max(raw[gr].z & 0x7fffu, (raw[gr].z >> 16) & 0x7fffu)),
-                  max(raw[gr].w & 0x7fffu, (raw[gr].w >> 16) & 0x7fffu));
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[gr].x & 0x7fff7fffu, raw[gr].y & 0x7fff7fffu),
+                                     __vmaxu2(raw[gr].z & 0x7fff7fffu, raw[gr].w & 0x7fff7fffu)));
       }
+      top = max(top & 0xffffu, top >> 16);
       top = max(top, __shfl_xor_sync(kFull, top, 1));
       top = max(top, __shfl_xor_sync(kFull, top, 2));
       // the row's largest value into [2^13, 2^14): a sixteenth of it, for the
@@ -407,35 +408,39 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
           sum += f[i];
         }
         // codes i and i + 4 share a register; 1, 3, 5, 7 stand 4 bits up
-        const uint32_t q[4] = {pack_f16x2(f[0], f[4]), pack_f16x2(f[1] * 0.0625f, f[5] * 0.0625f), pack_f16x2(f[2], f[6]),
-                               pack_f16x2(f[3] * 0.0625f, f[7] * 0.0625f)};
+        const uint4 q = make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1] * 0.0625f, f[5] * 0.0625f),
+                                   pack_f16x2(f[2], f[6]), pack_f16x2(f[3] * 0.0625f, f[7] * 0.0625f));
 #pragma unroll
         for (int i = 0; i < Q; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) qf[i][nt][gr][e] = HALF && g8 / 4 != i ? 0u : q[e];
+          reinterpret_cast<uint4*>(q_smem)[((i * NT + nt) * G + gr) * 32 + lane] =
+              HALF && g8 / 4 != i ? make_uint4(0, 0, 0, 0) : q;
         sum += __shfl_xor_sync(kFull, sum, 1);
         sum += __shfl_xor_sync(kFull, sum, 2);
         if (t4 == gr % 4) (gr < 4 ? mine : other) = sum * 5.9604644775390625e-8f;  // 2^-24
       }
 #pragma unroll
-      for (int m = 0; m < MINS; ++m) {
+      for (int m = 0; m < MINS; ++m) {  // three bf16 pieces of each sum
         const float s = m ? other : mine;
         const float h = hi16(__float_as_uint(s)), l = hi16(__float_as_uint(s - h));
+        const uint2 q = make_uint2(pack_bf16x2(h, l), pack_bf16x2((s - h) - l, 0.0f));
 #pragma unroll
-        for (int i = 0; i < Q; ++i) {
-          qmin[i][nt][m][0] = HALF && g8 / 4 != i ? 0u : pack_bf16x2(h, l);
-          qmin[i][nt][m][1] = HALF && g8 / 4 != i ? 0u : pack_bf16x2((s - h) - l, 0.0f);
-        }
+        for (int i = 0; i < Q; ++i)
+          reinterpret_cast<uint2*>(q_smem + C::kQ)[((i * NT + nt) * MINS + m) * 32 + lane] =
+              HALF && g8 / 4 != i ? make_uint2(0, 0) : q;
       }
       // above 0, for the product with a masked score
-      const float back = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(24 - k + 127) << 23), 1.17549435e-38f);
+      if (t4 == 0 && (!HALF || g8 < 4))
+        fac_smem[nt * 8 + g8] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(24 - k + 127) << 23), 1.17549435e-38f);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {  // the lane's columns 2 t4 + j
-        fac[nt][j] = __shfl_sync(kFull, back, 4 * (2 * t4 + j));
-        const int r = seg.rb * COLS + (nt * 8 + 2 * t4 + j) % COLS;
+        const int col = (nt * 8 + 2 * t4 + j) % COLS, r = seg.rb * COLS + col;
+        fac[nt][j] = fac_smem[col];
         limit[nt][j] = p.causal ? seg.s.len - seg.s.n + min(r / p.group, seg.s.n - 1) : seg.s.len - 1;
       }
-    }
     // every key up to this one is seen by all rows of the block
     const int all_see = p.causal ? seg.s.len - seg.s.n + seg.rb * COLS / p.group : seg.s.len - 1;
 
@@ -459,8 +464,9 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
       ok = ok && __all_sync(kFull, bounded_wait(bars + 8 * stage, phase, abort_flag, p.timeout_ns));
       if (!ok) break;
       --flying;
+      const uint32_t lost = bad & 3u;
+      bad >>= 2;
       const uint32_t rec = ring + stage * C::kStage;
-      const uint32_t lost = bad >> (2 * stage) & 3u;
       const bool edge = key - g8 + kPair * kKv4Tile - 1 > all_see || lost != 0;
 
       // halves of a pair of statistics that belong to cached tokens: of keys key + 16 i, + 8
@@ -490,7 +496,11 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
             if (HALF && edge) kl &= kept(i);  // a NaN would reach the other record's columns
             const uint32_t a0 = __byte_perm(kl, kl, 0x1010), a1 = __byte_perm(kl, kl, 0x3232);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_bf16_full(x[r][nt], a0, a1, a0, a1, qmin[i][nt][m][0], qmin[i][nt][m][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              uint32_t q0, q1;
+              lds_pair(q0, q1, qms + ((i * NT + nt) * MINS + m) * 256);
+              mma_bf16_full(x[r][nt], a0, a1, a0, a1, q0, q1);
+            }
           }
         }
         uint32_t ks[G];
@@ -506,14 +516,16 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
             const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+              uint32_t q[4];
+              lds_words<4>(q, qs + ((i * NT + nt) * G + gr) * 512);
               if (i == 0)
                 mma_f16_first(acc[nt], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u,
-                              qf[i][nt][gr][0], qf[i][nt][gr][1]);
+                              q[0], q[1]);
               else
                 mma_f16(acc[nt], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u,
-                        qf[i][nt][gr][0], qf[i][nt][gr][1]);
-              mma_f16(acc[nt], v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u, qf[i][nt][gr][2],
-                      qf[i][nt][gr][3]);
+                        q[0], q[1]);
+              mma_f16(acc[nt], v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u, q[2],
+                      q[3]);
             }
           }
 #pragma unroll
