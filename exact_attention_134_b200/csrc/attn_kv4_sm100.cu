@@ -121,6 +121,22 @@ __device__ __forceinline__ void mma_bf16_full(float (&c)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The four code operands of a word of 8 codes (bits 16 p + 4 n): n = 0 .. 3, the
+// odd ones 16 times their value. The last is a difference of fp16 numbers, off
+// the pipe that all the masks need.
+struct Codes {
+  uint32_t n[4];
+};
+__device__ __forceinline__ Codes codes_of(uint32_t w) {
+  Codes c;
+  c.n[0] = w & 0x000f000fu;
+  c.n[1] = w & 0x00f000f0u;
+  const uint32_t up = __byte_perm(w, 0u, 0x4341);
+  c.n[2] = up & 0x000f000fu;
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(c.n[3]) : "r"(up), "r"(c.n[2]));
+  return c;
+}
+
 // 8 x 8 transposition of 16-bit values over the warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -492,7 +508,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
           const uint32_t at = rec + (HALF ? i : r) * C::kRecord;
 #pragma unroll
           for (int m = 0; m < MINS; ++m) {
-            uint32_t kl = 4 * m + t4 < G ? lds_word(at + 17 * D + (g8 * G + 4 * m + t4) * 4) : 0u;
+            uint32_t kl = G % 4 == 0 || 4 * m + t4 < G ? lds_word(at + 17 * D + (g8 * G + 4 * m + t4) * 4) : 0u;
             if (HALF && edge) kl &= kept(i);  // a NaN would reach the other record's columns
             const uint32_t a0 = __byte_perm(kl, kl, 0x1010), a1 = __byte_perm(kl, kl, 0x3232);
 #pragma unroll
@@ -513,19 +529,14 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
           for (int i = 0; i < Q; ++i) {
             uint32_t w0, w1;
             lds_pair(w0, w1, rec + (HALF ? i : r) * C::kRecord + gr * 256 + lane * 8);
-            const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
+            const Codes c0 = codes_of(w0), c1 = codes_of(w1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               uint32_t q[4];
               lds_words<4>(q, qs + ((i * NT + nt) * G + gr) * 512);
-              if (i == 0)
-                mma_f16_first(acc[nt], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u,
-                              q[0], q[1]);
-              else
-                mma_f16(acc[nt], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u,
-                        q[0], q[1]);
-              mma_f16(acc[nt], v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u, q[2],
-                      q[3]);
+              if (i == 0) mma_f16_first(acc[nt], c0.n[0], c1.n[0], c0.n[1], c1.n[1], q[0], q[1]);
+              else mma_f16(acc[nt], c0.n[0], c1.n[0], c0.n[1], c1.n[1], q[0], q[1]);
+              mma_f16(acc[nt], c0.n[2], c1.n[2], c0.n[3], c1.n[3], q[2], q[3]);
             }
           }
 #pragma unroll
@@ -538,12 +549,12 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
         }
         lds_words<G>(vs[r], own + 18 * D + g8 * G * 4);
       }
+      // (lanes behind group G read the last one's again: rows that nothing uses)
       uint32_t vm[kPair][2];
 #pragma unroll
       for (int i = 0; i < kPair; ++i)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          vm[i][e] = g8 < G ? lds_word(rec + i * C::kRecord + 19 * D + g8 * 32 + 16 * e + t4 * 4) : 0u;
+        for (int e = 0; e < 2; ++e) vm[i][e] = lds_word(rec + i * C::kRecord + 19 * D + min(g8, G - 1) * 32 + 16 * e + t4 * 4);
       bool hidden = false;  // NaN scales beside keys that some row does not see
       if (edge) {
         // keys behind the cached ones hold anything: no scale or minimum of
@@ -628,6 +639,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
               o[nt][q][2 + j] *= f;
             }
             omin[nt][j] *= f;
+            if (HALF) omin[nt][2 + j] *= f;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
               pr[r][nt][j] = ex2_approx(fmaf(x[r][nt][j], fac[nt][j], -next));
@@ -636,9 +648,9 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
           }
       }
       // ---- O^T += V^T P^T
-      // with HALF an operand's columns of the other record are cleared
-      const uint32_t low = g8 < 4 ? 0xffffffffu : 0u;
-      auto of = [&](uint32_t v, int i) { return !HALF ? v : i ? v & ~low : v & low; };
+      // with HALF record 1's weights move to the rows' own columns; what record 0's
+      // and they leave in columns 4 .. 7 is never read
+      auto of = [&](uint32_t v, int i) { return i ? __shfl_xor_sync(kFull, v, 16) : v; };
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -654,11 +666,12 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
           const uint32_t l1 = transpose8(pack_bf16x2(pe[2] - lo16(h1), pe[3] - hi16(h1)));
           h0 = transpose8(h0);
           h1 = transpose8(h1);
-#pragma unroll
-          for (int i = 0; i < Q; ++i) {
-            const uint32_t(&v)[2] = vm[HALF ? i : r];
-            mma_bf16(omin[nt], v[0], v[1], of(h0, i), of(h1, i));
-            mma_bf16(omin[nt], v[0], v[1], of(l0, i), of(l1, i));
+          if (HALF) {  // rows 0 .. 7: record 0's minima, right in columns 0 .. 3; 8 .. 15: record 1's, in 4 .. 7
+            mma_bf16_full(omin[nt], vm[0][0], vm[1][0], vm[0][1], vm[1][1], h0, h1);
+            mma_bf16_full(omin[nt], vm[0][0], vm[1][0], vm[0][1], vm[1][1], l0, l1);
+          } else {
+            mma_bf16(omin[nt], vm[r][0], vm[r][1], h0, h1);
+            mma_bf16(omin[nt], vm[r][0], vm[r][1], l0, l1);
           }
         }
       auto values = [&](auto masked) {
@@ -684,12 +697,12 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
             for (int i = 0; i < Q; ++i) {
               uint32_t a, b;
               lds_pair(a, b, rec + (HALF ? i : r) * C::kRecord + 8 * D + gr * 256 + lane * 8);
-              const uint32_t a8 = a >> 8, b8 = b >> 8;
+              const Codes c0 = codes_of(a), c1 = codes_of(b);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 const uint32_t q0 = of(p0[nt], i), q1 = of(p1[nt], i);
-                mma_f16(o[nt][2 * gr], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u, q0, q1);
-                mma_f16(o[nt][2 * gr + 1], a8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x000f000fu, b8 & 0x00f000f0u, q0, q1);
+                mma_f16(o[nt][2 * gr], c0.n[0], c0.n[1], c1.n[0], c1.n[1], q0, q1);
+                mma_f16(o[nt][2 * gr + 1], c0.n[2], c0.n[3], c1.n[2], c1.n[3], q0, q1);
               }
             }
           }
@@ -713,12 +726,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         sum[0][j] += __shfl_xor_sync(kFull, sum[0][j], 2);
-        omin[0][j] += __shfl_xor_sync(kFull, omin[0][j], 2);
-#pragma unroll
-        for (int m = 0; m < 2 * G; ++m) {
-          o[0][m][j] += __shfl_xor_sync(kFull, o[0][m][j], 2);
-          o[0][m][2 + j] += __shfl_xor_sync(kFull, o[0][m][2 + j], 2);
-        }
+        omin[0][j] += __shfl_xor_sync(kFull, omin[0][2 + j], 2);
       }
     }
     const bool column = !HALF || t4 < 2;  // the lane's columns are rows
