@@ -4,34 +4,46 @@
 //   S_ij = scale * sum_g (s_jg * sum_{c in g} q_ic code_jc + lo_jg * sum_{c in g} q_ic)
 //   O_i  = sum_j p_ij (lo_jg + s_jg code_jc) / sum_j p_ij,  p_ij = 2^(S_ij log2(e) - R_i)
 // so the codes themselves are the operands of the matrix instructions and the
-// keys and values are never rounded: scale and minimum come in afterwards (K,
-// on the fp32 sums of a group) or before (V: p * s, one operand a group; the
-// minimum times p is one more, small product).
+// keys and values are never rounded: scale and minimum come in afterwards (K:
+// scale on the fp32 sums of a group, minima by one instruction against the
+// sums of the query's groups) or before (V: p * s, one operand a group; the
+// minima times p by one instruction).
 //
 // Operands. A code in the low bits of a 16-bit half is the fp16 subnormal
 // code * 2^-24, exact in the tensor core, and one 4 bits up is 16 times that:
-// a word of 8 codes becomes four operand registers with four ANDs and a shift.
-// The scores are taken as S^T = K Q^T (16 keys x 8 query rows an instruction)
-// and the output as O^T = V^T P^T: with one token and at most 8 query heads a
-// kv head, 8 columns hold the rows, where 64 or 128 rows of a tcgen05 tile
-// would be filled up with zeros, and operands go from the dequantised register
-// straight into the instruction; tcgen05 would need them written to shared or
-// tensor memory first. Q is scaled by a power of two a row into fp16's range;
-// P^T = p * s is fp16 as well, against a reference that follows the row's
-// maximum and the scales: p * s < 2^15.
+// a word of 8 codes becomes four operand registers with four masks and a
+// subtraction. The scores are taken as S^T = K Q^T (16 keys x 8 query rows an
+// instruction) and the output as O^T = V^T P^T: with one token and at most 8
+// query heads a kv head, 8 columns hold the rows, where 64 or 128 rows of a
+// tcgen05 tile would be filled up with zeros, and operands go from the
+// dequantised register straight into the instruction; tcgen05 would need them
+// written to shared or tensor memory first, and its accumulators read back for
+// the scale of every group. Q is scaled by a power of two a row into fp16's
+// range; P^T = p * s is fp16 as well (rounded once: 2^-12), against a reference
+// that follows the row's maximum and the keys' scales: p * s < 2^15. The minima
+// take p in two bf16 pieces (16 bits): they cancel against the codes' part.
 //
-// HBM-bound: 1.25 d bytes a cached token and kv head for K and V, against some
-// 260 warp instructions a record of 16 tokens (20 d = 2560 bytes at d = 128:
-// 111 clocks of an SM's share of the memory rate, 444 issue slots).
+// Work. A unit is a pair of records of one block of query rows (4, 8 or 16 of a
+// kv head); the units of all sequences, kv heads and row blocks form one list,
+// cut into equal ranges, one per CTA, whatever the lengths. The four warps of a
+// CTA take the units of a segment (the part of one row block in its range) in
+// turn, each with its own ring of bulk copies and its own softmax state; they
+// are joined in shared memory at the segment's end. A row block within one
+// range is written out there; one cut by a range's border leaves fp32 partial
+// results, which the merge kernel joins. Short caches are not cut (launch).
 //
-// Work. A unit is one record of one block of query rows; the units of all
-// sequences, kv heads and row blocks form one list, cut into equal ranges, one
-// per CTA, whatever the lengths. The warps of a CTA take the records of a
-// segment (the part of one row block in its range) in turn, each with its own
-// ring of bulk copies (one copy a record) and its own softmax state; they are
-// joined in shared memory at the segment's end. A row block within one range
-// is written out there; one cut by a range's border leaves fp32 partial
-// results, which the merge kernel joins.
+// What bounds it: 1.25 d bytes a cached token and kv head, and for up to 4 rows
+// 520 warp instructions a pair of records at d = 128 (5120 bytes: 222 clocks of
+// an SM's share of the memory rate, 888 issue slots). Measured (B200, one query
+// row of 32 / 8 heads, launches in a graph): 64 sequences of 4096 .. 8192 tokens
+// 98 us, 5.2 TB/s; one of 131072 44 us. From the first kernel on: a record a
+// step with minima on the FMA pipe 162 us; two records a step and minima by a
+// matrix instruction 137; four warps and three CTAs an SM instead of eight and
+// two 125; up to four rows against both records at once 112; query operands in
+// shared memory 110; the fourth operand by subtraction, weights moved instead of
+// masked 102. Five tiles of columns a warp, or a warp a tile on a shared ring,
+// were no faster for 40 rows (41 and 53 us against 37 with passes of 16): the
+// scales and weights of a row cost more than its share of the codes.
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -50,9 +62,6 @@ constexpr float kNone = -3.0e38f;     // reference of a row that has seen no key
 constexpr uint32_t kMinScale = 0x1f80u;  // bf16 2^-64: smaller scales count as that, so p stays below 2^79
 constexpr float kRoom = 32768.0f;     // p * s stays below 2^15
 constexpr float kHead = 8.0f;         // log2 of p * s at a new reference: 2^7 of room before the next one
-#ifndef KMU
-#define KMU 8
-#endif
 constexpr int kPair = 2;              // records of a step
 
 struct Kv4Params {
@@ -66,19 +75,19 @@ struct Kv4Params {
   int* status;
   int Hq, group;
   int causal;
+  int whole;           // units are whole row blocks: nothing to merge
   int min_units;       // smallest range worth a CTA
   float scale_log2;
   unsigned long long timeout_ns;
 };
 
+// CTAs of an SM: three where 168 registers a thread hold the accumulators.
+constexpr int kv4_ctas(int d, int cols) { return d <= 128 && d * cols <= 1024 ? 3 : 2; }
+
 template <int D, int COLS>
 struct Kv4Cfg {
-#ifndef KW
-#define KW 4
-#define KC 3
-#endif
-  static constexpr int kWarps = COLS <= 8 && D <= 128 ? KW : 4;
-  static constexpr int kCtasPerSm = D == 64 || (COLS <= 8 && D <= 128) ? KC : 2;
+  static constexpr int kWarps = 4;
+  static constexpr int kCtasPerSm = kv4_ctas(D, COLS);
   static constexpr int kStages = 2;
   static constexpr int kRecord = kv4_record_bytes(D);
   static constexpr int kStage = kPair * kRecord;
@@ -182,19 +191,25 @@ __device__ __forceinline__ uint32_t lds_word(uint32_t addr) {
   return a;
 }
 
+// Quotients of counts that mostly fit 32 bits.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // A sequence's part in the list of units: `blocks` row blocks for each kv
-// head, `units` for each of those (one per pair of records; one also for an
-// empty cache, so that its rows get their result).
+// head, `units` for each of those (one per pair of records, or one; one also
+// for an empty cache, so that its rows get their result).
 struct SeqWork {
-  int first, n, len, blocks, units;
+  int first, n, len, blocks, pairs, units;
 };
 template <int COLS>
 __device__ __forceinline__ SeqWork seq_work(const Kv4Params& p, int b) {
   SeqWork s;
   kv4_rows(p.c, b, s.first, s.n);
   s.len = kv4_len(p.c, b);
-  s.blocks = (int)(((long long)s.n * p.group + COLS - 1) / COLS);
-  s.units = max(1, (s.len + kPair * kKv4Tile - 1) / (kPair * kKv4Tile));
+  s.blocks = (int)(((uint32_t)s.n * (uint32_t)p.group + COLS - 1) / COLS);  // rows are below 2^31
+  s.pairs = max(1, (s.len + kPair * kKv4Tile - 1) / (kPair * kKv4Tile));
+  s.units = p.whole ? 1 : s.pairs;
   return s;
 }
 
@@ -204,7 +219,7 @@ __device__ __forceinline__ long long warp_sum(long long v) {
   return v;
 }
 
-// One segment: the units [t0, t1) of row block rb of kv head h of sequence b.
+// One segment: the pairs [t0, t1) of row block rb of kv head h of sequence b.
 struct Segment {
   int b, h, rb, t0, t1;
   SeqWork s;
@@ -234,10 +249,10 @@ __device__ __forceinline__ bool find_segment(const Kv4Params& p, long long u, Se
       g.b = b0 + l;
       g.s = seq_work<COLS>(p, g.b);
       const long long in = u - base - __shfl_sync(kFull, incl - mine, l);
-      const long long which = in / g.s.units;
-      g.t0 = (int)(in % g.s.units);
-      g.h = (int)(which / g.s.blocks);
-      g.rb = (int)(which % g.s.blocks);
+      const long long which = quotient(in, g.s.units);
+      g.t0 = (int)(in - which * g.s.units);
+      g.h = (int)quotient(which, g.s.blocks);
+      g.rb = (int)(which - (long long)g.h * g.s.blocks);
       return true;
     }
     base += __shfl_sync(kFull, incl, 31);
@@ -245,7 +260,13 @@ __device__ __forceinline__ bool find_segment(const Kv4Params& p, long long u, Se
   return false;
 }
 
-// Steps to the next segment of the list (its start; t1 is the caller's). False at the end.
+// Ends a segment with the range's `left` units, or its row block; returns the units behind it.
+__device__ __forceinline__ long long end_segment(const Kv4Params& p, Segment& g, long long left) {
+  g.t1 = p.whole ? g.s.pairs : (int)min((long long)g.s.pairs, g.t0 + left);
+  return left - (p.whole ? 1 : g.t1 - g.t0);
+}
+
+// Steps to the next segment of the list (its start). False at the end.
 template <int COLS>
 __device__ __forceinline__ bool next_segment(const Kv4Params& p, Segment& g) {
   g.t0 = 0;
@@ -271,7 +292,6 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
   // scores, weights and scales in the lanes stands for both records.
   constexpr bool HALF = COLS == 4;
   constexpr int NT = HALF ? 1 : COLS / 8;  // column tiles
-  constexpr int R = HALF ? 1 : kPair;      // sets of scores of a pair
   constexpr int Q = HALF ? kPair : 1;      // sets of query operands, by record
   constexpr int MINS = (G + 3) / 4;  // instructions for the minima of a record
   extern __shared__ __align__(128) uint8_t smem[];
@@ -304,16 +324,22 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
     }
   }
   total = warp_sum(total);
-  const long long ctas = max(1LL, min((long long)gridDim.x, total / p.min_units));
-  const long long begin = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
+  // equal ranges, the first `more` of them one unit longer
+  const long long ctas = max(1LL, min((long long)gridDim.x, quotient(total, p.min_units)));
+  const long long each = quotient(total, ctas), more = total - each * ctas;
+  const long long begin = each * blockIdx.x + min((long long)blockIdx.x, more);
+  const long long end = begin + each + ((long long)blockIdx.x < more ? 1 : 0);
   Segment seg;
   const bool any = blockIdx.x < ctas && begin < end && find_segment<COLS>(p, begin, seg);
-  if (threadIdx.x == 0) {
+  if (!p.whole && threadIdx.x == 0) {
     // a row block cut by this range's first border, and by none before: what the merge joins
     int4 a = make_int4(0, 0, 0, 0), z = a;
     if (any && seg.t0 > 0) {
-      const long long u0 = begin - seg.t0, u1 = u0 + seg.s.units - 1;
-      const int c0 = (int)(((u0 + 1) * ctas - 1) / total), c1 = (int)(((u1 + 1) * ctas - 1) / total);
+      const long long u0 = begin - seg.t0, u1 = u0 + seg.s.units - 1, border = more * (each + 1);
+      auto cta_of = [&](long long u) {
+        return (int)(u < border ? quotient(u, each + 1) : more + quotient(u - border, each));
+      };
+      const int c0 = cta_of(u0), c1 = cta_of(u1);
       if (c0 + 1 == (int)blockIdx.x) {
         a = make_int4(1, c0, c1, seg.h);
         z = make_int4(seg.rb, seg.s.first, seg.s.n, 0);
@@ -331,7 +357,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
   auto units = [&](const Segment& g) {  // of this warp in segment g (none of an empty cache)
     return g.s.len > 0 ? max(0, (g.t1 - g.t0 - warp + W - 1) / W) : 0;
   };
-  pf.t1 = (int)min((long long)pf.s.units, pf.t0 + pf_left);
+  pf_left = end_segment(p, pf, pf_left);
   int pf_k = 0, pf_count = units(pf);  // next unit of the warp in pf (t0 + warp + W * pf_k), and how many
   // of unit (pf_k / 32) * 32 + lane: its records, and the bytes to copy from
   // each (both from the first if they lie side by side)
@@ -345,10 +371,9 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
   auto issue = [&]() {
     while (pf_k >= pf_count) {
       if (!pf_more) return;
-      pf_left -= pf.t1 - pf.t0;
       pf_more = pf_left > 0 && next_segment<COLS>(p, pf);
       if (!pf_more) return;
-      pf.t1 = (int)min((long long)pf.s.units, pf_left);
+      pf_left = end_segment(p, pf, pf_left);
       pf_k = 0;
       pf_count = units(pf);
     }
@@ -384,7 +409,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
   for (int i = 0; i < S; ++i) issue();
 
   long long left = end - begin;
-  seg.t1 = (int)min((long long)seg.s.units, seg.t0 + left);
+  left = end_segment(p, seg, left);
   bool ok = true;
   int stage = 0;
   uint32_t phase = 0;
@@ -483,43 +508,43 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
       const uint32_t lost = bad & 3u;
       bad >>= 2;
       const uint32_t rec = ring + stage * C::kStage;
-      const bool edge = key - g8 + kPair * kKv4Tile - 1 > all_see || lost != 0;
-
       // halves of a pair of statistics that belong to cached tokens: of keys key + 16 i, + 8
       auto kept = [&](int i) {
         const int at = key + kKv4Tile * i, len = lost >> i & 1u ? 0 : seg.s.len;
         return (at < len ? 0x0000ffffu : 0u) | (at + 8 < len ? 0xffff0000u : 0u);
       };
-      // ---- scores
-      // the lane's keys in set r: of record r, or of its columns' record
-      const int mine_of = HALF ? t4 >> 1 : 0;
-      float x[R][NT][4];
-      uint32_t vs[R][G];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const uint32_t own = rec + (HALF ? mine_of : r) * C::kRecord;  // record of the lane's keys
+      // one record after the other, or with HALF both at once
+#pragma unroll 1
+      for (int r = 0; r < (HALF ? 1 : kPair); ++r) {
+        const uint32_t base = rec + r * C::kRecord;
+        const int mine_of = HALF ? t4 >> 1 : r;  // the record of the lane's columns
+        const uint32_t own = HALF ? rec + mine_of * C::kRecord : base;
+        const int last = key - g8 + kKv4Tile * (HALF ? kPair : r + 1) - 1;
+        const bool edge = last > all_see || lost != 0;
+
+        // ---- scores
+        float x[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[r][nt][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) x[nt][e] = 0.0f;
         // the minima of key g8 (+ 8) and group t4: once for each of two pieces of the sums
 #pragma unroll
-        for (int i = 0; i < Q; ++i) {
-          const uint32_t at = rec + (HALF ? i : r) * C::kRecord;
+        for (int i = 0; i < Q; ++i)
 #pragma unroll
           for (int m = 0; m < MINS; ++m) {
-            uint32_t kl = G % 4 == 0 || 4 * m + t4 < G ? lds_word(at + 17 * D + (g8 * G + 4 * m + t4) * 4) : 0u;
+            uint32_t kl = G % 4 == 0 || 4 * m + t4 < G
+                              ? lds_word(base + i * C::kRecord + 17 * D + (g8 * G + 4 * m + t4) * 4) : 0u;
             if (HALF && edge) kl &= kept(i);  // a NaN would reach the other record's columns
             const uint32_t a0 = __byte_perm(kl, kl, 0x1010), a1 = __byte_perm(kl, kl, 0x3232);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               uint32_t q0, q1;
               lds_pair(q0, q1, qms + ((i * NT + nt) * MINS + m) * 256);
-              mma_bf16_full(x[r][nt], a0, a1, a0, a1, q0, q1);
+              mma_bf16_full(x[nt], a0, a1, a0, a1, q0, q1);
             }
           }
-        }
-        uint32_t ks[G];
+        uint32_t ks[G], vs[G], vm[Q][2];
         lds_words<G>(ks, own + 16 * D + g8 * G * 4);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
@@ -528,7 +553,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
 #pragma unroll
           for (int i = 0; i < Q; ++i) {
             uint32_t w0, w1;
-            lds_pair(w0, w1, rec + (HALF ? i : r) * C::kRecord + gr * 256 + lane * 8);
+            lds_pair(w0, w1, base + i * C::kRecord + gr * 256 + lane * 8);
             const Codes c0 = codes_of(w0), c1 = codes_of(w1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -541,121 +566,99 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            x[r][nt][0] = fmaf(s0, acc[nt][0], x[r][nt][0]);
-            x[r][nt][1] = fmaf(s0, acc[nt][1], x[r][nt][1]);
-            x[r][nt][2] = fmaf(s1, acc[nt][2], x[r][nt][2]);
-            x[r][nt][3] = fmaf(s1, acc[nt][3], x[r][nt][3]);
+            x[nt][0] = fmaf(s0, acc[nt][0], x[nt][0]);
+            x[nt][1] = fmaf(s0, acc[nt][1], x[nt][1]);
+            x[nt][2] = fmaf(s1, acc[nt][2], x[nt][2]);
+            x[nt][3] = fmaf(s1, acc[nt][3], x[nt][3]);
           }
         }
-        lds_words<G>(vs[r], own + 18 * D + g8 * G * 4);
-      }
-      // (lanes behind group G read the last one's again: rows that nothing uses)
-      uint32_t vm[kPair][2];
+        lds_words<G>(vs, own + 18 * D + g8 * G * 4);
+        // (lanes behind group G read the last one's again: rows that nothing uses)
 #pragma unroll
-      for (int i = 0; i < kPair; ++i)
+        for (int i = 0; i < Q; ++i)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) vm[i][e] = lds_word(rec + i * C::kRecord + 19 * D + min(g8, G - 1) * 32 + 16 * e + t4 * 4);
-      bool hidden = false;  // NaN scales beside keys that some row does not see
-      if (edge) {
-        // keys behind the cached ones hold anything: no scale or minimum of
-        // theirs counts; keys that a row does not see get -inf
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const int i = HALF ? mine_of : r;
-          const int at = key + kKv4Tile * i;
-          const uint32_t keep = kept(i);
+          for (int e = 0; e < 2; ++e)
+            vm[i][e] = lds_word(base + i * C::kRecord + 19 * D + min(g8, G - 1) * 32 + 16 * e + t4 * 4);
+        bool hidden = false;  // NaN scales beside keys that some row does not see
+        if (edge) {
+          // keys behind the cached ones hold anything: no scale or minimum of
+          // theirs counts; keys that a row does not see get -inf
+          const int at = key + kKv4Tile * mine_of;
+          const uint32_t keep = kept(mine_of);
           uint32_t top = 0;
 #pragma unroll
           for (int gr = 0; gr < G; ++gr) {
-            vs[r][gr] &= keep;
-            top = __vmaxu2(top, vs[r][gr]);
+            vs[gr] &= keep;
+            top = __vmaxu2(top, vs[gr]);
           }
-          hidden |= (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u;
+          hidden = __any_sync(kFull, (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (at + (e & 2) * 4 > limit[nt][e & 1] || !(keep >> (e & 2) * 8 & 1u)) x[r][nt][e] = -INFINITY;
+              if (at + (e & 2) * 4 > limit[nt][e & 1] || !(keep >> (e & 2) * 8 & 1u)) x[nt][e] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < Q; ++i) {
+            const int which = HALF ? i : r;
+            const int pair = key - g8 + kKv4Tile * which + 2 * t4, len = lost >> which & 1u ? 0 : seg.s.len;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              vm[i][e] &= (pair + 8 * e < len ? 0x0000ffffu : 0u) | (pair + 8 * e + 1 < len ? 0xffff0000u : 0u);
+          }
         }
-#pragma unroll
-        for (int i = 0; i < kPair; ++i) {
-          const int pair = key - g8 + kKv4Tile * i + 2 * t4, len = lost >> i & 1u ? 0 : seg.s.len;
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            vm[i][e] &= (pair + 8 * e < len ? 0x0000ffffu : 0u) | (pair + 8 * e + 1 < len ? 0xffff0000u : 0u);
-        }
-        hidden = __any_sync(kFull, hidden);
-      }
-      // ---- weights; a new reference where p * s would pass 2^15. The bound of s
-      // is each key's own, over its groups
-      float pr[R][NT][4];
-      bool over = false;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
+        // ---- weights; a new reference where p * s would pass 2^15. The bound of s
+        // is each key's own, over its groups
+        float pr[NT][4];
+        bool over = false;
         uint32_t top = kMinScale | kMinScale << 16;
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) top = __vmaxu2(top, vs[r][gr]);
-        const float s0 = lo16(top), s1 = hi16(top);
+        for (int gr = 0; gr < G; ++gr) top = __vmaxu2(top, vs[gr]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) pr[r][nt][e] = ex2_approx(fmaf(x[r][nt][e], fac[nt][e & 1], -ref[nt][e & 1]));
-          const float m0 = fmaxf(pr[r][nt][0], pr[r][nt][1]) * s0, m1 = fmaxf(pr[r][nt][2], pr[r][nt][3]) * s1;
+          for (int e = 0; e < 4; ++e) pr[nt][e] = ex2_approx(fmaf(x[nt][e], fac[nt][e & 1], -ref[nt][e & 1]));
+          const float m0 = fmaxf(pr[nt][0], pr[nt][1]) * lo16(top), m1 = fmaxf(pr[nt][2], pr[nt][3]) * hi16(top);
           over |= !(m0 < kRoom) || !(m1 < kRoom);  // NaN scales too
         }
-      }
-      if (__any_sync(kFull, over)) {
-        float bound[R][2];  // log2 of the keys' scales, NaN ones left out
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          uint32_t t0 = kMinScale, t1 = kMinScale;
+        if (__any_sync(kFull, over)) {
+          uint32_t t0 = kMinScale, t1 = kMinScale;  // NaN scales left out
 #pragma unroll
           for (int gr = 0; gr < G; ++gr) {
-            const uint32_t a = vs[r][gr] & 0xffffu, b = vs[r][gr] >> 16;
+            const uint32_t a = vs[gr] & 0xffffu, b = vs[gr] >> 16;
             t0 = max(t0, a < 0x7f80u ? a : 0u);
             t1 = max(t1, b < 0x7f80u ? b : 0u);
           }
-          bound[r][0] = (float)((int)(t0 >> 7) - 126);
-          bound[r][1] = (float)((int)(t1 >> 7) - 126);
+          const float b0 = (float)((int)(t0 >> 7) - 126), b1 = (float)((int)(t1 >> 7) - 126);  // log2 of the keys' scales
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float m = fmaxf(kNone, fmaxf(fmaf(x[nt][j], fac[nt][j], b0), fmaf(x[nt][2 + j], fac[nt][j], b1)));
+              if (HALF) m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));  // one reference for a row's two columns
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+              const float next = fmaxf(ref[nt][j], m - kHead);
+              const float f = ex2_approx(ref[nt][j] - next);
+              ref[nt][j] = next;
+              sum[nt][j] *= f;
+#pragma unroll
+              for (int q = 0; q < 2 * G; ++q) {
+                o[nt][q][j] *= f;
+                o[nt][q][2 + j] *= f;
+              }
+              omin[nt][j] *= f;
+              if (HALF) omin[nt][2 + j] *= f;
+              pr[nt][j] = ex2_approx(fmaf(x[nt][j], fac[nt][j], -next));
+              pr[nt][2 + j] = ex2_approx(fmaf(x[nt][2 + j], fac[nt][j], -next));
+            }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float m = kNone;
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-              m = fmaxf(m, fmaxf(fmaf(x[r][nt][j], fac[nt][j], bound[r][0]), fmaf(x[r][nt][2 + j], fac[nt][j], bound[r][1])));
-            if (HALF) m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));  // one reference for a row's two columns
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-            const float next = fmaxf(ref[nt][j], m - kHead);
-            const float f = ex2_approx(ref[nt][j] - next);
-            ref[nt][j] = next;
-            sum[nt][j] *= f;
-#pragma unroll
-            for (int q = 0; q < 2 * G; ++q) {
-              o[nt][q][j] *= f;
-              o[nt][q][2 + j] *= f;
-            }
-            omin[nt][j] *= f;
-            if (HALF) omin[nt][2 + j] *= f;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              pr[r][nt][j] = ex2_approx(fmaf(x[r][nt][j], fac[nt][j], -next));
-              pr[r][nt][2 + j] = ex2_approx(fmaf(x[r][nt][2 + j], fac[nt][j], -next));
-            }
-          }
-      }
-      // ---- O^T += V^T P^T
-      // with HALF record 1's weights move to the rows' own columns; what record 0's
-      // and they leave in columns 4 .. 7 is never read
-      auto of = [&](uint32_t v, int i) { return i ? __shfl_xor_sync(kFull, v, 16) : v; };
-#pragma unroll
-      for (int r = 0; r < R; ++r)
+        // ---- O^T += V^T P^T
+        // with HALF record 1's weights move to the rows' own columns; what record 0's
+        // and they leave in columns 4 .. 7 is never read
+        auto of = [&](uint32_t v, int i) { return i ? __shfl_xor_sync(kFull, v, 16) : v; };
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float(&pe)[4] = pr[r][nt];
+          const float(&pe)[4] = pr[nt];
           sum[nt][0] += pe[0] + pe[2];
           sum[nt][1] += pe[1] + pe[3];
           // the minimum's weights in two bf16 steps (16 bits): the minimum and
@@ -667,49 +670,48 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
           h0 = transpose8(h0);
           h1 = transpose8(h1);
           if (HALF) {  // rows 0 .. 7: record 0's minima, right in columns 0 .. 3; 8 .. 15: record 1's, in 4 .. 7
-            mma_bf16_full(omin[nt], vm[0][0], vm[1][0], vm[0][1], vm[1][1], h0, h1);
-            mma_bf16_full(omin[nt], vm[0][0], vm[1][0], vm[0][1], vm[1][1], l0, l1);
+            mma_bf16_full(omin[nt], vm[0][0], vm[Q - 1][0], vm[0][1], vm[Q - 1][1], h0, h1);
+            mma_bf16_full(omin[nt], vm[0][0], vm[Q - 1][0], vm[0][1], vm[Q - 1][1], l0, l1);
           } else {
-            mma_bf16(omin[nt], vm[r][0], vm[r][1], h0, h1);
-            mma_bf16(omin[nt], vm[r][0], vm[r][1], l0, l1);
+            mma_bf16(omin[nt], vm[0][0], vm[0][1], h0, h1);
+            mma_bf16(omin[nt], vm[0][0], vm[0][1], l0, l1);
           }
         }
-      auto values = [&](auto masked) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
+        auto values = [&](auto masked) {
 #pragma unroll
           for (int gr = 0; gr < G; ++gr) {
-            const float s0 = lo16(vs[r][gr]), s1 = hi16(vs[r][gr]);
-            uint32_t p0[NT], p1[NT];
+            const float s0 = lo16(vs[gr]), s1 = hi16(vs[gr]);
+            Codes c0[Q], c1[Q];
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+              uint32_t a, b;
+              lds_pair(a, b, base + i * C::kRecord + 8 * D + gr * 256 + lane * 8);
+              c0[i] = codes_of(a);
+              c1[i] = codes_of(b);
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const float(&pe)[4] = pr[r][nt];
+              const float(&pe)[4] = pr[nt];
               float w[4] = {pe[0] * s0, pe[1] * s0, pe[2] * s1, pe[3] * s1};
               if (decltype(masked)::value) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if (x[r][nt][e] == -INFINITY) w[e] = 0.0f;
+                  if (x[nt][e] == -INFINITY) w[e] = 0.0f;
               }
-              p0[nt] = transpose8(pack_f16x2(w[0], w[1]));
-              p1[nt] = transpose8(pack_f16x2(w[2], w[3]));
-            }
+              const uint32_t p0 = transpose8(pack_f16x2(w[0], w[1])), p1 = transpose8(pack_f16x2(w[2], w[3]));
 #pragma unroll
-            for (int i = 0; i < Q; ++i) {
-              uint32_t a, b;
-              lds_pair(a, b, rec + (HALF ? i : r) * C::kRecord + 8 * D + gr * 256 + lane * 8);
-              const Codes c0 = codes_of(a), c1 = codes_of(b);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint32_t q0 = of(p0[nt], i), q1 = of(p1[nt], i);
-                mma_f16(o[nt][2 * gr], c0.n[0], c0.n[1], c1.n[0], c1.n[1], q0, q1);
-                mma_f16(o[nt][2 * gr + 1], c0.n[2], c0.n[3], c1.n[2], c1.n[3], q0, q1);
+              for (int i = 0; i < Q; ++i) {
+                const uint32_t q0 = of(p0, i), q1 = of(p1, i);
+                mma_f16(o[nt][2 * gr], c0[i].n[0], c0[i].n[1], c1[i].n[0], c1[i].n[1], q0, q1);
+                mma_f16(o[nt][2 * gr + 1], c0[i].n[2], c0[i].n[3], c1[i].n[2], c1[i].n[3], q0, q1);
               }
             }
           }
-      };
-      // a NaN group reaches only the rows that see its key
-      if (!hidden) values(std::false_type());
-      else values(std::true_type());
+        };
+        // a NaN group reaches only the rows that see its key
+        if (!hidden) values(std::false_type());
+        else values(std::true_type());
+      }
       // ---- the stage is free
       __syncwarp();
       issue();
@@ -771,7 +773,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
       }
       __syncthreads();
     }
-    const bool whole = seg.t0 == 0 && seg.t1 == seg.s.units;
+    const bool whole = seg.t0 == 0 && seg.t1 == seg.s.pairs;
     const size_t slot = 2 * (size_t)blockIdx.x + (seg.t0 > 0 ? 0 : 1);
     for (int i = threadIdx.x; i < COLS * (D / 4); i += W * 32) {
       const int col = i / (D / 4), c4 = i % (D / 4);
@@ -802,9 +804,8 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
           p.lse[(size_t)head * p.c.total + tok] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
       }
     }
-    left -= seg.t1 - seg.t0;
     if (left <= 0 || !next_segment<COLS>(p, seg)) break;
-    seg.t1 = (int)min((long long)seg.s.units, left);
+    left = end_segment(p, seg, left);
     turn ^= 1;
   }
   if (!ok) {  // its own copies in flight still land in this shared memory
@@ -872,12 +873,20 @@ __global__ void __launch_bounds__(kMergeThreads) attn_kv4_merge_kernel(const __g
   if (c4 == 0) p.lse[(size_t)head * p.c.total + tok] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
 }
 
-// Rows of a kv head in one pass over its records: 4, 8, or 16 columns by the
-// rows that a sequence has (at d = 256 the accumulators of 16 do not fit).
-int row_cols(int d, long long rows) { return rows <= 4 ? 4 : rows <= 8 || d > 128 ? 8 : 16; }
+// Most column tiles of 8 rows in one pass over a kv head's records: as many as
+// their accumulators leave registers for.
+constexpr int max_tiles(int d) { return d <= 128 ? 2 : 1; }
+
+// Columns for a sequence's rows: 4, or the tiles that share them evenly among
+// the fewest passes.
+int row_cols(int d, long long rows) {
+  if (rows <= 4) return 4;
+  const long long tiles = (rows + 7) / 8, passes = (tiles + max_tiles(d) - 1) / max_tiles(d);
+  return 8 * (int)((tiles + passes - 1) / passes);
+}
 
 // Most CTAs of a launch: those that are resident at once.
-int max_ctas(int d, int cols) { return 148 * (d == 64 || (cols <= 8 && d <= 128) ? KC : 2); }
+int max_ctas(int d, int cols) { return 148 * kv4_ctas(d, cols); }
 
 struct Kv4Workspace {
   size_t rl, split, total;
@@ -898,7 +907,7 @@ cudaError_t launch_kv4(const Kv4Params& p, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   attn_kv4_kernel<D, COLS><<<ctas, C::kWarps * 32, C::kSmemBytes, stream>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || ctas == 1) return e;
+  if (e != cudaSuccess || ctas == 1 || p.whole) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas - 1);
   cfg.blockDim = dim3(kMergeThreads);
@@ -914,7 +923,7 @@ cudaError_t launch_kv4(const Kv4Params& p, int ctas, cudaStream_t stream) {
 template <int D>
 cudaError_t launch_cols(const Kv4Params& p, int cols, int ctas, cudaStream_t stream) {
   if (cols == 4) return launch_kv4<D, 4>(p, ctas, stream);
-  if constexpr (D <= 128) {
+  if constexpr (max_tiles(D) >= 2) {
     if (cols == 16) return launch_kv4<D, 16>(p, ctas, stream);
   }
   return launch_kv4<D, 8>(p, ctas, stream);
@@ -963,12 +972,19 @@ attn_status_t attn_fwd_kv4(const void* q, const void* pool, const int* page_tabl
   p.Hq = Hq;
   p.group = Hq / Hkv;
   p.causal = causal;
-  p.min_units = KMU;
+  // Short caches are not split: a merge and its launch take longer than the
+  // pairs, or than their last ones where the row blocks fill the GPU. One query
+  // row of 32 / 8 heads, whole / split (us): 500 tokens, 1 sequence 10.4 / 10.4,
+  // 4 10.4 / 14.6, 64 20.6 / 24.7, 250 50 / 61; 1000 tokens, 1 14.5 / 11.0,
+  // 4 14.5 / 15.0, 64 28.8 / 30.8, 250 74 / 82; 2000 tokens, 64 46 / 43, 250 119 / 115
+  const long long pairs = std::max(1LL, ((long long)max_pages * page_size + kPair * kKv4Tile - 1) / (kPair * kKv4Tile));
+  const long long row_blocks = std::max<long long>(num_seqs, (long long)total_q * p.group / cols) * Hkv;
+  p.whole = pairs <= 16 || (pairs <= 32 && row_blocks >= 2 * 148);
+  p.min_units = p.whole ? 1 : 8;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.timeout_ns = wait_budget_ns();
   // no more CTAs than the longest possible caches have ranges
-  const long long most = ((long long)total_q * p.group / cols + num_seqs) * Hkv *
-                         std::max(1LL, ((long long)max_pages * page_size + kPair * kKv4Tile - 1) / (kPair * kKv4Tile));
+  const long long most = ((long long)total_q * p.group / cols + num_seqs) * Hkv * (p.whole ? 1 : pairs);
   const int ctas = (int)std::max(1LL, std::min<long long>(max_ctas(d, cols), most / p.min_units));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
