@@ -11,7 +11,7 @@ missing or cannot run, the call raises.
     dq, dk, dv = attn_bwd(q, k, v, o, lse, do, causal=True)
     o = attention(q, k, v, causal=True); o.backward(do)  # torch autograd
 
-Before it and beside it: norm_rope.py (per-head norm and rotation of queries and
+Before it and beside it: rope.py (per-head norm and rotation of queries and
 keys), kv4.py (the paged 4-bit key/value cache and attention over it),
 kv4_pages.py (the host's bookkeeping of its pages).
 """
@@ -130,13 +130,14 @@ def _call(name, index, *args):
     there), the device's current stream as its last argument, and checks its status."""
     import torch
     fn = getattr(_lib or lib(), name)
-    here = torch.cuda.current_device()
-    if here == index:
+    # the raw calls behind current_device() and current_stream(): those cost as much as a launch
+    if torch._C._cuda_getDevice() == index:
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
             status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    _check(status, name)
+    if status:
+        _check(status, name)
 
 
 def _shape_args(q, k, v):
@@ -600,4 +601,4 @@ def version() -> int:
 from .kv4 import (attn_fwd_kv4, fwd_kv4_workspace_size, kv4_alloc, kv4_append, kv4_copy_pages,  # noqa: E402
                   kv4_gather, kv4_page_bytes)
 from .kv4_pages import KV4Pages, OutOfPages, page_pairs  # noqa: E402
-from .norm_rope import norm_rope, qk_norm_rope, qk_norm_rope_bwd  # noqa: E402
+from .rope import norm_rope, qk_norm_rope, qk_norm_rope_bwd  # noqa: E402

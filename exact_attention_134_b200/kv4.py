@@ -47,11 +47,15 @@ def _cache_args(pool, page_table, seq_lens, cu_seqlens, d=None):
     shape = pool.shape
     if pool.dtype is not torch.uint8 or index < 0 or len(shape) != 4 or shape[3] % 20 or not pool.is_contiguous():
         raise ValueError("pool must be a contiguous uint8 CUDA tensor [num_pages, Hkv, page_size / 16, 20 d]")
-    for name, t, dim in (("page_table", page_table, 2), ("seq_lens", seq_lens, 1), ("cu_seqlens", cu_seqlens, 1)):
-        if t is None and dim == 1 and name == "cu_seqlens":
-            continue
-        if t.dtype is not torch.int32 or t.get_device() != index or t.dim() != dim or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {dim} dimension(s) on the pool's device")
+    i32 = torch.int32
+    if page_table.dtype is not i32 or page_table.get_device() != index or page_table.dim() != 2 or \
+            not page_table.is_contiguous():
+        raise ValueError("page_table must be a contiguous int32 CUDA tensor [num_seqs, max_pages] on the pool's device")
+    if seq_lens.dtype is not i32 or seq_lens.get_device() != index or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be a contiguous int32 CUDA vector on the pool's device")
+    if cu_seqlens is not None and (cu_seqlens.dtype is not i32 or cu_seqlens.get_device() != index or
+                                   cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous()):
+        raise ValueError("cu_seqlens must be a contiguous int32 CUDA vector on the pool's device")
     num_pages, Hkv, tiles, record = shape
     n, max_pages = page_table.shape
     if seq_lens.shape[0] != n:
@@ -83,13 +87,12 @@ def kv4_append(k, v, pool, page_table, seq_lens, cu_seqlens=None):
     n, max_pages, num_pages, page_size, pool_heads, _, index = _cache_args(pool, page_table, seq_lens, cu_seqlens, d)
     if Hkv != pool_heads:
         raise ValueError(f"the pool holds {pool_heads} kv heads, not {Hkv}")
-    strides = []
-    for name, t in (("k", k), ("v", v)):
-        s = t.stride()
-        if t.dtype is not torch.bfloat16 or t.get_device() != index or (s[2] != 1 and d > 1):
-            raise ValueError(f"{name} must be a bf16 CUDA tensor with contiguous channels on the pool's device")
-        # the stride of an axis of one is never used: torch leaves anything there
-        strides += (s[0] if total > 1 else 0, s[1] if Hkv > 1 else 0)
+    sk, sv, bf16 = k.stride(), v.stride(), torch.bfloat16
+    if k.dtype is not bf16 or v.dtype is not bf16 or k.get_device() != index or v.get_device() != index or \
+            ((sk[2] != 1 or sv[2] != 1) and d > 1):
+        raise ValueError("k and v must be bf16 CUDA tensors with contiguous channels on the pool's device")
+    # the stride of an axis of one is never used: torch leaves anything there
+    strides = (sk[0] if total > 1 else 0, sk[1] if Hkv > 1 else 0, sv[0] if total > 1 else 0, sv[1] if Hkv > 1 else 0)
     _call("attn_kv4_append", index, k.data_ptr(), v.data_ptr(), *strides, pool.data_ptr(), page_table.data_ptr(),
           seq_lens.data_ptr(), _ptr(cu_seqlens), n, max_pages, num_pages, page_size, total, Hkv, d)
 
@@ -106,7 +109,7 @@ def kv4_gather(pool, page_table, seq_lens, total: int, cu_seqlens=None, k=None, 
         if t is not None and (t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape or
                               not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor {shape} on the pool's device")
-    k = torch.empty(shape, dtype=torch.bfloat16, device=pool.device) if k is None else k
+    k = pool.new_empty(shape, dtype=torch.bfloat16) if k is None else k
     v = torch.empty_like(k) if v is None else v
     _call("attn_kv4_gather", index, pool.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_seqlens), n,
           max_pages, num_pages, page_size, shape[0], Hkv, d, k.data_ptr(), v.data_ptr())
@@ -168,16 +171,16 @@ def attn_fwd_kv4(q, pool, page_table, seq_lens, cu_seqlens_q=None, max_seqlen_q:
     elif out.dtype is not torch.bfloat16 or out.get_device() != index or out.shape != shape or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bf16 CUDA tensor {tuple(shape)} on the device of q")
     if lse is None:
-        lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((Hq, total), dtype=torch.float32)
     elif lse.dtype is not torch.float32 or lse.get_device() != index or lse.shape != (Hq, total) or \
             not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous fp32 CUDA tensor {(Hq, total)} on the device of q")
     if workspace is None:
-        workspace = torch.empty(fwd_kv4_workspace_size(Hq, Hkv, max_seqlen_q, d), dtype=torch.uint8, device=q.device)
+        workspace = lse.new_empty((fwd_kv4_workspace_size(Hq, Hkv, max_seqlen_q, d) // 4,))
     elif workspace.get_device() != index:
         raise ValueError("workspace must be on the device of q")
     _call("attn_fwd_kv4", index, q.data_ptr(), pool.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
           _ptr(cu_seqlens_q), out.data_ptr(), lse.data_ptr(), n, max_pages, num_pages, page_size, int(max_seqlen_q),
           total, Hq, Hkv, d, 1 if causal else 0, float(scale), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+          workspace.nbytes)
     return out, lse

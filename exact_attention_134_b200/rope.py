@@ -14,9 +14,11 @@ from __future__ import annotations
 
 import struct
 
-from . import _c_int, _call, lib
+from . import _call, lib
 
+# arrays of long long and int as the C calls read them
 _pack12, _pack18 = struct.Struct("12q").pack, struct.Struct("18q").pack
+_pack_ints = [None] + [struct.Struct(f"{n}i").pack for n in range(1, 5)]
 
 
 def _ptr(t):
@@ -55,7 +57,7 @@ def _rows(name, t, shape, index, written=False):
     else:
         B, (N, H, _) = 1, shape
         r = (0, s[1] if H > 1 else 0, s[0] if N > 1 else 0)
-    if written and 0 in r and any(n > 1 and x == 0 for n, x in zip((B, H, N), r)):
+    if written and ((H > 1 and r[1] == 0) or (N > 1 and r[2] == 0) or (B > 1 and r[0] == 0)):
         raise ValueError(f"{name} is written to and must not be expanded")
     return r
 
@@ -91,7 +93,7 @@ def _rotation(positions, inv_freq, sections, B, N, packed, index):
         raise ValueError(f"positions {shape} do not fit {axes} axes, batch {B} and {N} tokens")
     if N > 1 and stride[-1] != 1:
         raise ValueError("positions must be contiguous along the tokens")
-    return p.data_ptr(), axis, batch, inv_freq.data_ptr(), (_c_int * axes)(*sections), axes, 2 * half
+    return p.data_ptr(), axis, batch, inv_freq.data_ptr(), _pack_ints[axes](*sections), axes, 2 * half
 
 
 def _weights(q_weight, k_weight, d, index):
@@ -111,9 +113,17 @@ def _weights(q_weight, k_weight, d, index):
     return int(dtype is torch.bfloat16)
 
 
-def _new(t):
+def _written(name, t, like, index):
+    """The tensor to write a result in the shape of `like` to, a new contiguous one if None, and its strides."""
     import torch
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
+    if t is not None:
+        return t, _rows(name, t, like.shape, index, True)
+    t = torch.empty_like(like) if like.is_contiguous() else torch.empty_like(like, memory_format=torch.contiguous_format)
+    if t.dim() == 4:
+        _, H, N, d = t.shape
+        return t, (H * N * d, N * d, d)
+    _, H, d = t.shape
+    return t, (0, d, H * d)
 
 
 def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -140,10 +150,9 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
     strides = _rows("q", q, q.shape, index) + _rows("k", k, k.shape, index)
     rot = _rotation(positions, inv_freq, sections, B, N, q.dim() == 3, index)
     bf16 = _weights(q_weight, k_weight, d, index)
-    q_out = _new(q) if q_out is None else q_out
-    k_out = _new(k) if k_out is None else k_out
-    strides += _rows("q_out", q_out, q.shape, index, True) + _rows("k_out", k_out, k.shape, index, True)
-    _call("attn_qk_norm_rope", index, q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _pack12(*strides),
+    q_out, sq = _written("q_out", q_out, q, index)
+    k_out, sk = _written("k_out", k_out, k, index)
+    _call("attn_qk_norm_rope", index, q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _pack12(*strides, *sq, *sk),
           _ptr(q_weight), _ptr(k_weight), bf16, *rot, 1 if interleaved else 0, B, N, Hq, Hkv, d, float(eps))
     return q_out, k_out
 
@@ -169,24 +178,25 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, positions=None, inv_freq=None, q_weig
     strides = _rows("q", q, q.shape, index) + _rows("k", k, k.shape, index)
     rot = _rotation(positions, inv_freq, sections, B, N, q.dim() == 3, index)
     bf16 = _weights(q_weight, k_weight, d, index)
-    dq = _new(q) if dq is None else dq
-    dk = _new(k) if dk is None else dk
-    strides += _rows("dq_out", dq_out, q.shape, index) + _rows("dk_out", dk_out, k.shape, index) + \
-        _rows("dq", dq, q.shape, index, True) + _rows("dk", dk, k.shape, index, True)
+    strides += _rows("dq_out", dq_out, q.shape, index) + _rows("dk_out", dk_out, k.shape, index)
+    dq, sq = _written("dq", dq, q, index)
+    dk, sk = _written("dk", dk, k, index)
     dwq = dwk = None
     nbytes = 0
     if norm:
-        dwq, dwk = (torch.empty(d, dtype=torch.float32, device=q.device) for _ in range(2))
+        if bf16:
+            dwq, dwk = (torch.empty_like(q_weight, dtype=torch.float32) for _ in range(2))
+        else:
+            dwq, dwk = torch.empty_like(q_weight), torch.empty_like(q_weight)
         if workspace is None:
-            workspace = torch.empty(int(lib().attn_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hkv, d)),
-                                    dtype=torch.uint8, device=q.device)
+            workspace = dwq.new_empty((lib().attn_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hkv, d) // 4,))
         elif workspace.get_device() != index:
             raise ValueError("workspace must be on the device of q")
-        nbytes = workspace.numel() * workspace.element_size()
+        nbytes = workspace.nbytes
     else:
         workspace = None
     _call("attn_qk_norm_rope_bwd", index, q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),
-          dq.data_ptr(), dk.data_ptr(), _pack18(*strides), _ptr(q_weight), _ptr(k_weight), bf16, _ptr(dwq), _ptr(dwk),
+          dq.data_ptr(), dk.data_ptr(), _pack18(*strides, *sq, *sk), _ptr(q_weight), _ptr(k_weight), bf16, _ptr(dwq), _ptr(dwk),
           *rot, 1 if interleaved else 0, B, N, Hq, Hkv, d, float(eps), _ptr(workspace), nbytes)
     return dq, dk, dwq, dwk
 
