@@ -52,7 +52,7 @@
 
 #include "attn_internal.h"
 #include "kv4_format.cuh"
-#include "sm100_ptx.cuh"
+#include "sm100_rows.cuh"
 
 namespace attn_sm100 {
 namespace {
@@ -158,9 +158,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-
-__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // N consecutive words of shared memory, in the widest loads their alignment allows.
 template <int N>

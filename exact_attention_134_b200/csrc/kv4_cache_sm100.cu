@@ -28,7 +28,7 @@
 
 #include "attn_internal.h"
 #include "kv4_format.cuh"
-#include "sm100_ptx.cuh"
+#include "sm100_rows.cuh"
 
 namespace attn_sm100 {
 namespace {
@@ -64,9 +64,6 @@ __device__ __forceinline__ uint32_t swap_pair(uint32_t w, bool odd) {
   const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w : w >> 16, 4);
   return odd ? __byte_perm(got, w, 0x7610) : __byte_perm(w, got, 0x5410);
 }
-
-__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // min and max of packed bf16 pairs; NaN if one of them is
 __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {

@@ -30,7 +30,7 @@
 #include <algorithm>
 
 #include "attn_internal.h"
-#include "sm100_ptx.cuh"
+#include "sm100_rows.cuh"
 
 namespace attn_sm100 {
 namespace {
@@ -180,22 +180,23 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdBlocksPerSm : kFwdBlocksPe
            : p.w_bf16      ? __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p.w[part]) + c) << 16)
                            : __ldg(static_cast<const float*>(p.w[part]) + c);
   };
-  auto token = [&](int group, int& b, int& n) {  // the last one in place of those behind it
+  auto token = [&](int group, int& b, int& n) {  // false behind the last one (which stands in)
     const int row = min(group * kRows + sub, rows - 1);
     b = row / p.N;
     n = row - b * p.N;
+    return group * kRows + sub < rows;
   };
 
   const long long hx = p.xs[part][1], hdy = BWD ? p.dys[part][1] : 0, hy = p.ys[part][1];
   int group = (int)(begin / heads), h = (int)(begin % heads), b, n;
   int next_group = group, next_h = h, stage = 0, next_stage = 0;
-  token(group, b, n);
+  bool copies = token(group, b, n) && holds;  // rows behind the last are not read: another warp may write in place
   const uint16_t* x = p.x[part] + b * p.xs[part][0] + n * p.xs[part][2] + h * hx + 8 * lane;
   const uint16_t* dy = BWD ? p.dy[part] + b * p.dys[part][0] + n * p.dys[part][2] + h * hdy + 8 * lane : nullptr;
   auto fetch = [&]() {
     if (ahead > 0) {
       --ahead;
-      if (holds) {
+      if (copies) {
         const uint32_t at = to + next_stage * kStep;
         if (!BWD || norm) {
           cp_async16(at, x);
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdBlocksPerSm : kFwdBlocksPe
       if (++next_h == heads) {
         next_h = 0;
         int b_, n_;
-        token(++next_group, b_, n_);
+        copies = token(++next_group, b_, n_) && holds;
         x = p.x[part] + b_ * p.xs[part][0] + n_ * p.xs[part][2] + 8 * lane;
         if (BWD) dy = p.dy[part] + b_ * p.dys[part][0] + n_ * p.dys[part][2] + 8 * lane;
       }
@@ -237,8 +238,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdBlocksPerSm : kFwdBlocksPe
   const int over = 8 * (c1 - c0);
   for (; left > 0; --left) {
     if (fresh) {  // another group of tokens
-      token(group, b, n);
-      live = group * kRows + sub < rows;
+      live = token(group, b, n);
       y = p.y[part] + b * p.ys[part][0] + n * p.ys[part][2] + h * hy + 8 * c0;
       if (turns) angles<INTER>(p, c0, c1, b, n, cs, sn);
       fresh = false;
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdBlocksPerSm : kFwdBlocksPe
     if (BWD)
       unpack<INTER>(*reinterpret_cast<const uint4*>(s_x + 1024 + 16 * c0),
                     *reinterpret_cast<const uint4*>(s_x + 1024 + 16 * c1), g);
-    if (!holds) {  // nothing was copied there
+    if (!holds || !live) {  // nothing was copied there
 #pragma unroll
       for (int i = 0; i < 4; ++i) v.a[i] = v.b[i] = g.a[i] = g.b[i] = both(0.0f);
     }
@@ -397,6 +397,11 @@ void launch_rope(const RopeParams& p, const RopeGrid& g, int d, cudaStream_t str
 
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Whether the result at y may be written while x is read: another tensor, or x itself with its own strides.
+bool apart(const void* x, const long long* xs, const void* y, const long long* ys) {
+  return x != y || (xs[0] == ys[0] && xs[1] == ys[1] && xs[2] == ys[2]);
+}
+
 // The checks and parameters that both directions share. tensors: q, k, then
 // for each further pair as the caller lists them (strides in the same order).
 attn_status_t rope_params(RopeParams* p, const void* const* tensors, int num_tensors, const long long* strides,
@@ -476,6 +481,7 @@ attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q_out, void*
       rope_params(&p, t, 4, strides, q_weight, k_weight, weight_bf16, positions, pos_axis_stride, pos_batch_stride,
                   inv_freq, sections, num_axes, rotary_dim, interleaved, B, N, Hq, Hkv, d, eps);
   if (s != ATTN_OK) return s;
+  if (!apart(q, strides, q_out, strides + 6) || !apart(k, strides + 3, k_out, strides + 9)) return ATTN_ERR_INVALID_ARG;
   p.x[0] = static_cast<const uint16_t*>(q);
   p.x[1] = static_cast<const uint16_t*>(k);
   p.y[0] = static_cast<uint16_t*>(q_out);
@@ -507,6 +513,8 @@ attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq
       rope_params(&p, t, 6, strides, q_weight, k_weight, weight_bf16, positions, pos_axis_stride, pos_batch_stride,
                   inv_freq, sections, num_axes, rotary_dim, interleaved, B, N, Hq, Hkv, d, eps);
   if (s != ATTN_OK) return s;
+  if (!apart(dq_out, strides + 6, dq, strides + 12) || !apart(dk_out, strides + 9, dk, strides + 15))
+    return ATTN_ERR_INVALID_ARG;
   if (q_weight) {
     if (!dq_weight || !dk_weight) return ATTN_ERR_INVALID_ARG;
     if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4)) return ATTN_ERR_ALIGNMENT;

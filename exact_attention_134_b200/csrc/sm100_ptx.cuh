@@ -424,21 +424,6 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// ---------------------------------------------------------------- plain asynchronous copies
-// 16 bytes from global to shared memory, both 16-byte aligned; a lane waits for
-// its own groups, the warp's copies need a __syncwarp() behind that.
-__device__ __forceinline__ void cp_async16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-// All but the last N groups of the lane have landed.
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // ---------------------------------------------------------------- packed fp32 (sm_100)
 __device__ __forceinline__ uint64_t f2_bits(float2 a) {
   uint64_t r;
@@ -455,12 +440,6 @@ __device__ __forceinline__ float2 bits_f2(uint64_t r) {
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
-  return bits_f2(r);
-}
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
   return bits_f2(r);
 }
 

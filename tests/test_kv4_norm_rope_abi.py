@@ -21,7 +21,7 @@ def lib():
 def _rope(lib, bwd=False, t=None, strides=None, wq=P, wk=P, bf16=0, pos=P, pa=0, pb=0, freq=P, sec=(64,), axes=None,
           rot=128, inter=0, B=2, N=100, Hq=4, Hkv=2, d=128, eps=1e-6, dwq=P, dwk=P, ws=P, nbytes=None):
     n = 6 if bwd else 4
-    t = [P] * n if t is None else t
+    t = [P + 0x1000 * i for i in range(n)] if t is None else t
     strides = [512, 128, 512] * n if strides is None else strides
     s = (LL * len(strides))(*strides) if strides else None
     sec_ = (INT * max(len(sec), 1))(*sec) if sec is not None else None
@@ -48,11 +48,54 @@ def test_norm_rope_validation(lib, bwd, kw, code):
     assert _rope(lib, bwd, **kw) == code
 
 
+def test_norm_rope_in_place_needs_the_same_strides(lib):
+    """A result may be the tensor it is made of, with its strides only."""
+    for bwd, x, y in ((False, 0, 2), (False, 1, 3), (True, 2, 4), (True, 3, 5)):
+        n = 6 if bwd else 4
+        t = [P + 0x1000 * i for i in range(n)]
+        t[y] = t[x]
+        s = [512, 128, 512] * n
+        s[3 * y + 1] = 256
+        assert _rope(lib, bwd, t=t, strides=s) == 1
+
+
+def test_calls_are_made_on_the_tensors_device(monkeypatch):
+    """With another device current, a call switches to the tensors' one and back."""
+    seen, at = [], [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            at[0] = self.index
+
+        def __exit__(self, *exc):
+            at[0] = 0
+
+    class Lib:
+        @staticmethod
+        def entry(*args):
+            seen.append((at[0], args))
+            return 1 if args[0] == "bad" else 0
+
+    monkeypatch.setattr(attn, "_lib", Lib)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: at[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 100 + index, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    attn._call("entry", 0, 7)
+    attn._call("entry", 3, 8)
+    assert seen == [(0, (7, 100)), (3, (8, 103))] and at[0] == 0
+    with pytest.raises(attn.AttnError):
+        attn._call("entry", 2, "bad")
+    assert at[0] == 0
+
+
 @pytest.mark.parametrize("bwd", [False, True])
 def test_norm_rope_tensor_validation(lib, bwd):
     n = 6 if bwd else 4
     for i in range(n):
-        t = [P] * n
+        t = [P + 0x1000 * i for i in range(n)]
         t[i] = None
         assert _rope(lib, bwd, t=t) == 1
         t[i] = P + 8
