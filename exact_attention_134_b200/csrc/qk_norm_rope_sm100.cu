@@ -21,9 +21,9 @@
 // arithmetic and loads straight into registers: 75 us forwards, 133 backwards
 // where the bytes take 51 and 77), hence packed fp32x2 arithmetic, 16 values a
 // lane against the loop's overhead, and rows copied ahead into shared memory
-// by cp.async, which keeps 96 KB an SM in flight without registers.
-// Measured (B200, one launch in a graph): 2 x 8192 x 40 heads of 128, forwards
-// 61 us (5.5 TB/s), backwards 89 us (5.7 TB/s, both launches).
+// by cp.async, which keeps 48 KB an SM in flight without registers.
+// Measured (B200, one call behind the other): 2 x 8192 x 40 heads of 128,
+// forwards 63 us (5.3 TB/s), backwards 88 us (5.7 TB/s, both launches).
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -35,13 +35,17 @@
 namespace attn_sm100 {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kMaxAxes = 4;
-// blocks of an SM and steps in a warp's ring. Measured (us), forwards 2 x 8192
-// x 40 heads of 128: 6 x 4 61, 6 x 6 61, 5 x 6 63, 8 x 4 63; backwards 4 x 3 89,
-// 3 x 4 89, 4 x 5 91, 5 x 3 (40 bytes of spills) 95.
-constexpr int kFwdBlocksPerSm = 6, kFwdRing = 4;
-constexpr int kBwdBlocksPerSm = 4, kBwdRing = 3;
+// Blocks of an SM and steps in a warp's ring. Large blocks and little in flight
+// keep a block's rows together in DRAM; more of either is slower once every
+// call's results are written back behind the next one's reads. Measured, one
+// call behind the other (us), threads x blocks, ring: forwards 2 x 8192 x 40
+// heads of 128: 128 x 6, 4 69.9; 256 x 3, 4 69.9; 256 x 3, 2 66.0; 256 x 2, 2
+// 63.6; 256 x 2, 3 62.9; 256 x 2, 4 66.0; 512 x 1, 2 64.7; backwards: 128 x 4, 3
+// 98.6; 256 x 2, 3 96.2; 256 x 2, 2 87.7; 256 x 2, 1 98.5; 384 x 1, 2 89.2.
+constexpr int kFwdBlocksPerSm = 2, kFwdRing = 3;
+constexpr int kBwdBlocksPerSm = 2, kBwdRing = 2;
 
 struct RopeParams {
   const uint16_t* x[2];    // q, k: bf16 rows (batch, head, token strides below)
