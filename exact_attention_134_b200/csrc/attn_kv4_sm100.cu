@@ -81,8 +81,12 @@ struct Kv4Params {
   unsigned long long timeout_ns;
 };
 
-// CTAs of an SM: three where 168 registers a thread hold the accumulators.
-constexpr int kv4_ctas(int d, int cols) { return d <= 128 && d * cols <= 1024 ? 3 : 2; }
+// CTAs of an SM: four where 128 registers a thread hold the accumulators (64
+// sequences of 16384 tokens, 8 kv heads of 64, 4 / 8 rows: 121 / 148 us, with
+// three 126 / 156), three where 168 do.
+constexpr int kv4_ctas(int d, int cols) {
+  return d == 64 && cols <= 8 ? 4 : d <= 128 && d * cols <= 1024 ? 3 : 2;
+}
 
 template <int D, int COLS>
 struct Kv4Cfg {
@@ -291,6 +295,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
   constexpr int NT = HALF ? 1 : COLS / 8;  // column tiles
   constexpr int Q = HALF ? kPair : 1;      // sets of query operands, by record
   constexpr int MINS = (G + 3) / 4;  // instructions for the minima of a record
+  constexpr int kUnroll = C::kCtasPerSm == 4 ? 1 : 2;  // a pair's records side by side: 2 % where registers last
   extern __shared__ __align__(128) uint8_t smem[];
   float* const join = reinterpret_cast<float*>(smem + C::kRing);
   float2* const rl = reinterpret_cast<float2*>(smem + C::kRing + C::kJoin);
@@ -511,7 +516,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
         return (at < len ? 0x0000ffffu : 0u) | (at + 8 < len ? 0xffff0000u : 0u);
       };
       // one record after the other, or with HALF both at once
-#pragma unroll 1
+#pragma unroll kUnroll
       for (int r = 0; r < (HALF ? 1 : kPair); ++r) {
         const uint32_t base = rec + r * C::kRecord;
         const int mine_of = HALF ? t4 >> 1 : r;  // the record of the lane's columns

@@ -295,7 +295,8 @@ def test_values_of_unusual_size(what):
     _check(q, pool, rows, [n], [0, 1], 1, 64, True, d ** -0.5, o, lse)
 
 
-def test_a_row_sees_no_nan_behind_its_mask():
+@pytest.mark.parametrize("heads", [1, 2, 6])
+def test_a_row_sees_no_nan_behind_its_mask(heads):
     """Keys and values of NaN reach the rows that see them, and no others; what a record
     holds behind the last token (anything at all) reaches none."""
     g = torch.Generator().manual_seed(12)
@@ -304,7 +305,7 @@ def test_a_row_sees_no_nan_behind_its_mask():
     kn, vn = k.clone(), v.clone()
     kn[36, 0, 3] = float("nan")
     vn[35, 0, 40] = float("inf")
-    q = torch.randn((3, 2, d), generator=g).bfloat16()
+    q = torch.randn((3, heads, d), generator=g).bfloat16()
     pool = torch.full((3, 1, 1, 20 * d), 0xff, dtype=torch.uint8, device="cuda")   # scales and minima of NaN
     clean = torch.zeros_like(pool)
     table, lens = _ints([[0, 1, 2]]), _ints([n])
@@ -317,16 +318,21 @@ def test_a_row_sees_no_nan_behind_its_mask():
     assert o[2].isnan().all() and lse[:, 2].isnan().all()
 
 
-def test_bad_pages_are_left_out_and_reported():
+@pytest.mark.parametrize("Hq,page", [(4, 16), (4, 64), (12, 32), (20, 16)])
+def test_bad_pages_are_left_out_and_reported(Hq, page):
     lens = [70, 20]
-    pool, rows, _, _ = _filled(lens, 2, 64, 16, seed=13)
-    q = torch.randn((2, 4, 64), generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    pool, rows, _, _ = _filled(lens, 2, 64, page, seed=13)
+    q = torch.randn((2, Hq, 64), generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    at = min(2, len(rows[0]) - 1)
     want, wl = attn.attn_fwd_kv4(q[1:], pool, _ints(rows[1:]), _ints(lens[1:]))
     for bad in (pool.shape[0], -1, 2 ** 31 - 1, -2 ** 31):
-        broken = [[*rows[0][:2], bad, *rows[0][3:]], rows[1]]
+        broken = [[*rows[0][:at], bad, *rows[0][at + 1:]], rows[1]]
         o, lse = attn.attn_fwd_kv4(q, pool, _ints(broken), _ints(lens))
         assert attn.get_status() == (1, 0x500)
         assert o[0].isfinite().all() and torch.equal(o[1:], want) and torch.equal(lse[:, 1:], wl)
+        if at * page + page >= lens[0]:  # the last page: as if the sequence ended before it
+            short, sl = attn.attn_fwd_kv4(q[:1], pool, _ints(rows[:1]), _ints([at * page]))
+            assert torch.equal(o[:1], short) and torch.equal(lse[:, :1], sl)
     assert attn.get_status() == (0, 0)
 
 
