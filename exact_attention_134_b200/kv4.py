@@ -137,7 +137,7 @@ def kv4_copy_pages(pool, src, dst):
 
 
 def fwd_kv4_workspace_size(Hq: int, Hkv: int, max_seqlen_q: int, d: int) -> int:
-    """Bytes of scratch that attn_fwd_kv4 needs (8 MB at most; any number of sequences)."""
+    """Bytes of scratch that attn_fwd_kv4 needs (5 MB at most; any number of sequences)."""
     return int(lib().attn_fwd_kv4_workspace_size(Hq, Hkv, int(max_seqlen_q), d))
 
 

@@ -454,7 +454,7 @@ ATTN_API attn_status_t attn_qk_norm_rope_bwd(
  * tokens, 5 bits a value: for every token, kv head and group of 32 channels a
  * bf16 minimum lo and scale s and 4-bit codes, standing for lo + s * code with
  *     lo = min_c x_c,  s = bf16((max_c x_c - lo) / 15),
- *     code_c = min(rne((x_c - lo) / s), 15).
+ *     code_c = min(rne((x_c - lo) / s), 15), x_c - lo and the quotient in fp32.
  * A group with a spread below 15 * 2^-125 is held as its minimum (s = 2^-13 |lo|
  * then, 0 if that is below 2^-125); a group with a NaN or an infinity is held as
  * NaN.
@@ -534,15 +534,16 @@ ATTN_API attn_status_t attn_kv4_copy_pages(void* pool, int num_layers, int num_p
  *            sequence stand at its last tokens; with causal = 1 row i of n sees
  *            tokens 0 .. seq_lens - n + i, with causal = 0 all of them. A row
  *            that sees none gets O = 0 and LSE = -inf
- *   max_seqlen_q  bounds every sequence's query rows: it chooses between 8 and
+ *   max_seqlen_q  bounds every sequence's query rows: it chooses 4, 8 or
  *            16 rows a pass (a larger sequence is computed all the same)
  *   workspace  device scratch of attn_fwd_kv4_workspace_size() bytes, 16-byte
  *            aligned, for one call at a time; needs no initial value
- * Any number of query rows is computed, 8 or 16 (row, head) pairs of a kv head
+ * Any number of query rows is computed, 4, 8 or 16 (row, head) pairs of a kv head
  * in one pass over its cache; for long chunks attn_kv4_gather and
  * attn_fwd_varlen are faster. |v| up to 2^64; a token's groups whose scale is
- * below 2^-20 of its largest lose precision. Two launches (attention, merge of
- * what was split); allocates nothing; deterministic.
+ * below 2^-20 of its largest lose precision. One launch where page_table holds
+ * at most 512 tokens a sequence (1024 with many sequences), else two (attention,
+ * merge of what was split); allocates nothing; deterministic.
  */
 ATTN_API size_t attn_fwd_kv4_workspace_size(int Hq, int Hkv, int max_seqlen_q, int d);
 ATTN_API attn_status_t attn_fwd_kv4(const void* q, const void* pool, const int* page_table,
