@@ -63,6 +63,7 @@ constexpr uint32_t kMinScale = 0x1f80u;  // bf16 2^-64: smaller scales count as 
 constexpr float kRoom = 32768.0f;     // p * s stays below 2^15
 constexpr float kHead = 8.0f;         // log2 of p * s at a new reference: 2^7 of room before the next one
 constexpr int kPair = 2;              // records of a step
+constexpr int kAlwaysWhole = 16;      // pairs (512 tokens) that are one CTA's work in every launch
 
 struct Kv4Params {
   Kv4Pool c;
@@ -959,8 +960,20 @@ attn_status_t attn_fwd_kv4(const void* q, const void* pool, const int* page_tabl
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(lse)) & 15u)
     return ATTN_ERR_ALIGNMENT;
   const int cols = row_cols(d, (long long)max_seqlen_q * (Hq / Hkv));
+  p.group = Hq / Hkv;
+  // Short caches are not split: a merge and its launch take longer than the
+  // pairs, or than their last ones where the row blocks fill the GPU. One query
+  // row of 32 / 8 heads, whole / split (us): 500 tokens, 1 sequence 10.4 / 10.4,
+  // 4 10.4 / 14.6, 64 20.6 / 24.7, 250 50 / 61; 1000 tokens, 1 14.5 / 11.0,
+  // 4 14.5 / 15.0, 64 28.8 / 30.8, 250 74 / 82; 2000 tokens, 64 46 / 43, 250 119 / 115
+  const long long pairs = std::max(1LL, ((long long)max_pages * page_size + kPair * kKv4Tile - 1) / (kPair * kKv4Tile));
+  const long long row_blocks = std::max<long long>(num_seqs, (long long)total_q * p.group / cols) * Hkv;
+  p.whole = pairs <= kAlwaysWhole || (pairs <= 32 && row_blocks >= 2 * 148);
   const Kv4Workspace w = workspace(d, cols);
-  if (!workspace_ptr || (reinterpret_cast<uintptr_t>(workspace_ptr) & 15u) || workspace_bytes < w.total)
+  // the partial results' only; caches of kAlwaysWhole pairs never leave any
+  const bool unused = pairs <= kAlwaysWhole && !workspace_ptr;
+  if (!unused &&
+      (!workspace_ptr || (reinterpret_cast<uintptr_t>(workspace_ptr) & 15u) || workspace_bytes < w.total))
     return ATTN_ERR_WORKSPACE;
   p.status = device_status_word();
   if (!p.status) return ATTN_ERR_CUDA;
@@ -972,16 +985,7 @@ attn_status_t attn_fwd_kv4(const void* q, const void* pool, const int* page_tabl
   p.part_rl = reinterpret_cast<float2*>(ws + w.rl);
   p.split = reinterpret_cast<int4*>(ws + w.split);
   p.Hq = Hq;
-  p.group = Hq / Hkv;
   p.causal = causal;
-  // Short caches are not split: a merge and its launch take longer than the
-  // pairs, or than their last ones where the row blocks fill the GPU. One query
-  // row of 32 / 8 heads, whole / split (us): 500 tokens, 1 sequence 10.4 / 10.4,
-  // 4 10.4 / 14.6, 64 20.6 / 24.7, 250 50 / 61; 1000 tokens, 1 14.5 / 11.0,
-  // 4 14.5 / 15.0, 64 28.8 / 30.8, 250 74 / 82; 2000 tokens, 64 46 / 43, 250 119 / 115
-  const long long pairs = std::max(1LL, ((long long)max_pages * page_size + kPair * kKv4Tile - 1) / (kPair * kKv4Tile));
-  const long long row_blocks = std::max<long long>(num_seqs, (long long)total_q * p.group / cols) * Hkv;
-  p.whole = pairs <= 16 || (pairs <= 32 && row_blocks >= 2 * 148);
   p.min_units = p.whole ? 1 : 8;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.timeout_ns = wait_budget_ns();

@@ -152,7 +152,8 @@ def attn_fwd_kv4(q, pool, page_table, seq_lens, cu_seqlens_q=None, max_seqlen_q:
     max_seqlen_q: the longest sequence's query rows (a bound of them chooses the
     kernel; total_q / num_seqs, rounded up, when not given). workspace: a uint8
     cuda buffer of fwd_kv4_workspace_size(Hq, Hkv, max_seqlen_q, d) bytes, one
-    for each call that may run at the same time (allocated here if None).
+    for each call that may run at the same time (allocated here if None and the
+    table holds more than 512 tokens a sequence, which need it).
     Returns (o bf16 [total_q, Hq, d], lse fp32 [Hq, total_q]); a row that sees no
     token gets o = 0 and lse = -inf.
     """
@@ -175,12 +176,12 @@ def attn_fwd_kv4(q, pool, page_table, seq_lens, cu_seqlens_q=None, max_seqlen_q:
     elif lse.dtype is not torch.float32 or lse.get_device() != index or lse.shape != (Hq, total) or \
             not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous fp32 CUDA tensor {(Hq, total)} on the device of q")
-    if workspace is None:
+    if workspace is None and max_pages * page_size > 512:  # shorter caches leave no partial results
         workspace = lse.new_empty((fwd_kv4_workspace_size(Hq, Hkv, max_seqlen_q, d) // 4,))
-    elif workspace.get_device() != index:
+    elif workspace is not None and workspace.get_device() != index:
         raise ValueError("workspace must be on the device of q")
     _call("attn_fwd_kv4", index, q.data_ptr(), pool.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
           _ptr(cu_seqlens_q), out.data_ptr(), lse.data_ptr(), n, max_pages, num_pages, page_size, int(max_seqlen_q),
-          total, Hq, Hkv, d, 1 if causal else 0, float(scale), workspace.data_ptr(),
-          workspace.nbytes)
+          total, Hq, Hkv, d, 1 if causal else 0, float(scale), _ptr(workspace),
+          0 if workspace is None else workspace.nbytes)
     return out, lse

@@ -537,7 +537,8 @@ ATTN_API attn_status_t attn_kv4_copy_pages(void* pool, int num_layers, int num_p
  *   max_seqlen_q  bounds every sequence's query rows: it chooses 4, 8 or
  *            16 rows a pass (a larger sequence is computed all the same)
  *   workspace  device scratch of attn_fwd_kv4_workspace_size() bytes, 16-byte
- *            aligned, for one call at a time; needs no initial value
+ *            aligned, for one call at a time; needs no initial value. May be
+ *            NULL where page_table holds at most 512 tokens a sequence
  * Any number of query rows is computed, 4, 8 or 16 (row, head) pairs of a kv head
  * in one pass over its cache; for long chunks attn_kv4_gather and
  * attn_fwd_varlen are faster. |v| up to 2^64; a token's groups whose scale is

@@ -514,6 +514,7 @@ def test_refusals():
                          (lambda: attn.attn_fwd_kv4(q[:, :3].contiguous(), pool, table, lens), 1),
                          (lambda: attn.attn_fwd_kv4(q, pool, table, lens, scale=0.0), 1),
                          (lambda: attn.attn_fwd_kv4(q, pool, table, lens, workspace=small), 6),
+                         (lambda: attn.attn_fwd_kv4(q, pool, _ints([[0] * 33] * 2), lens, workspace=small), 6),
                          (lambda: attn.kv4_copy_pages(pool, lens[:0], lens[:0]), 1)):
         with pytest.raises(attn.AttnError) as e:
             call()

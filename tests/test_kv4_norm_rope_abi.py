@@ -164,7 +164,8 @@ def test_fwd_kv4_validation(lib):
         for mq in (1, 8, 64):
             need = lib.attn_fwd_kv4_workspace_size(16, 8, mq, d)
             assert 0 < need < 16 << 20 and need % 256 == 0
-            kw = dict(d=d, mq=mq)
+            kw = dict(d=d, mq=mq, mp=9)  # 576 tokens: partial results are possible
+            assert _fwd(lib, ws=P + 8, nbytes=need, d=d, mq=mq) == 6  # one that is given is checked
             assert _fwd(lib, ws=None, **kw) == 6 and _fwd(lib, ws=P + 8, **kw) == 6 and _fwd(lib, nbytes=need - 1, **kw) == 6
     assert lib.attn_fwd_kv4_workspace_size(12, 8, 1, 128) == 0 and lib.attn_fwd_kv4_workspace_size(16, 8, 0, 128) == 0
     assert lib.attn_fwd_kv4_workspace_size(16, 8, 1, 80) == 0
