@@ -205,9 +205,11 @@ _AUTOGRAD_FN = None
 
 
 def _readable(t):
-    """A gradient as the kernel can read it (autograd hands over any strides)."""
+    """A gradient as the kernel can read it (autograd hands over any strides, and
+    views that begin anywhere: contiguous() would return such a one as it is)."""
+    import torch
     ok = t.stride(-1) == 1 and all(s % 8 == 0 for s in t.stride()[:-1]) and t.data_ptr() % 16 == 0
-    return t if ok else t.contiguous()
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
 
 
 def _autograd_fn():

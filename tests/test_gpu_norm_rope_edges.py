@@ -1,0 +1,35 @@
+"""Calls of the norm with rotation at the edges of what its documentation allows."""
+import pytest
+import torch
+
+import exact_attention_134_b200 as attn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    attn.lib()
+
+
+def _inputs(N, Hq, Hkv, d, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    q, k = (torch.randn((N, h, d), generator=g).bfloat16().cuda() for h in (Hq, Hkv))
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")
+    inv = (1e4 ** (-torch.arange(d // 2).float() / (d // 2))).cuda()
+    wq, wk = ((1 + 0.1 * torch.randn(d, generator=g)).cuda() for _ in range(2))
+    return q, k, pos, inv, wq, wk
+
+
+def test_a_gradient_that_begins_off_a_16_byte_boundary():
+    """A result joined behind three other values hands back a contiguous gradient 6 bytes off."""
+    q, k, pos, inv, wq, wk = _inputs(9, 4, 2, 64)
+    dy = torch.randn((3 + q.numel(),), device="cuda").bfloat16()
+    want = attn.qk_norm_rope_bwd(q, k, dy[3:].view(q.shape).clone(), torch.zeros_like(k), pos, inv, wq, wk)
+    leaves = [t.detach().requires_grad_() for t in (q, k, wq, wk)]
+    yq, _ = attn.norm_rope(leaves[0], leaves[1], pos, inv, *leaves[2:])
+    torch.cat([torch.zeros(3, device="cuda").bfloat16(), yq.flatten()]).backward(dy)
+    for got, ref in zip(leaves, want):
+        assert torch.equal(got.grad, ref)
