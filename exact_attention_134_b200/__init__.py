@@ -140,6 +140,15 @@ def _call(name, index, *args):
         _check(status, name)
 
 
+def _changed(*tensors):
+    """Tells autograd that a call wrote to the caller's own tensors (None: not
+    given), so that a backward that saved one of them raises its usual error."""
+    import torch
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def _shape_args(q, k, v):
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k, v must be [B, H, N, d]")

@@ -21,7 +21,7 @@ from __future__ import annotations
 
 import math
 
-from . import _call, lib
+from . import _call, _changed, lib
 
 
 def kv4_page_bytes(Hkv: int, d: int, page_size: int) -> int:
@@ -95,6 +95,7 @@ def kv4_append(k, v, pool, page_table, seq_lens, cu_seqlens=None):
     strides = (sk[0] if total > 1 else 0, sk[1] if Hkv > 1 else 0, sv[0] if total > 1 else 0, sv[1] if Hkv > 1 else 0)
     _call("attn_kv4_append", index, k.data_ptr(), v.data_ptr(), *strides, pool.data_ptr(), page_table.data_ptr(),
           seq_lens.data_ptr(), _ptr(cu_seqlens), n, max_pages, num_pages, page_size, total, Hkv, d)
+    _changed(pool)
 
 
 def kv4_gather(pool, page_table, seq_lens, total: int, cu_seqlens=None, k=None, v=None):
@@ -109,10 +110,12 @@ def kv4_gather(pool, page_table, seq_lens, total: int, cu_seqlens=None, k=None, 
         if t is not None and (t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape or
                               not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor {shape} on the pool's device")
+    given = k, v
     k = pool.new_empty(shape, dtype=torch.bfloat16) if k is None else k
     v = torch.empty_like(k) if v is None else v
     _call("attn_kv4_gather", index, pool.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_seqlens), n,
           max_pages, num_pages, page_size, shape[0], Hkv, d, k.data_ptr(), v.data_ptr())
+    _changed(*given)
     return k, v
 
 
@@ -134,6 +137,7 @@ def kv4_copy_pages(pool, src, dst):
     layers, num_pages, H, tiles, record = shape if len(shape) == 5 else (1, *shape)
     _call("attn_kv4_copy_pages", index, pool.data_ptr(), layers, num_pages, H * tiles * record, src.data_ptr(),
           dst.data_ptr(), n)
+    _changed(pool)
 
 
 def fwd_kv4_workspace_size(Hq: int, Hkv: int, max_seqlen_q: int, d: int) -> int:
@@ -167,6 +171,7 @@ def attn_fwd_kv4(q, pool, page_table, seq_lens, cu_seqlens_q=None, max_seqlen_q:
         scale = 1.0 / math.sqrt(d)
     if max_seqlen_q is None:
         max_seqlen_q = -(-total // max(n, 1))
+    given = out, lse
     if out is None:
         out = torch.empty_like(q)
     elif out.dtype is not torch.bfloat16 or out.get_device() != index or out.shape != shape or not out.is_contiguous():
@@ -184,4 +189,5 @@ def attn_fwd_kv4(q, pool, page_table, seq_lens, cu_seqlens_q=None, max_seqlen_q:
           _ptr(cu_seqlens_q), out.data_ptr(), lse.data_ptr(), n, max_pages, num_pages, page_size, int(max_seqlen_q),
           total, Hq, Hkv, d, 1 if causal else 0, float(scale), _ptr(workspace),
           0 if workspace is None else workspace.nbytes)
+    _changed(*given)
     return out, lse

@@ -14,7 +14,7 @@ from __future__ import annotations
 
 import struct
 
-from . import _call, lib
+from . import _call, _changed, lib
 
 # arrays of long long and int as the C calls read them
 _pack12, _pack18 = struct.Struct("12q").pack, struct.Struct("18q").pack
@@ -150,10 +150,12 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
     strides = _rows("q", q, q.shape, index) + _rows("k", k, k.shape, index)
     rot = _rotation(positions, inv_freq, sections, B, N, q.dim() == 3, index)
     bf16 = _weights(q_weight, k_weight, d, index)
+    given = q_out, k_out
     q_out, sq = _written("q_out", q_out, q, index)
     k_out, sk = _written("k_out", k_out, k, index)
     _call("attn_qk_norm_rope", index, q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _pack12(*strides, *sq, *sk),
           _ptr(q_weight), _ptr(k_weight), bf16, *rot, 1 if interleaved else 0, B, N, Hq, Hkv, d, float(eps))
+    _changed(*given)
     return q_out, k_out
 
 
@@ -179,6 +181,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, positions=None, inv_freq=None, q_weig
     rot = _rotation(positions, inv_freq, sections, B, N, q.dim() == 3, index)
     bf16 = _weights(q_weight, k_weight, d, index)
     strides += _rows("dq_out", dq_out, q.shape, index) + _rows("dk_out", dk_out, k.shape, index)
+    given = dq, dk
     dq, sq = _written("dq", dq, q, index)
     dk, sk = _written("dk", dk, k, index)
     dwq = dwk = None
@@ -198,6 +201,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, positions=None, inv_freq=None, q_weig
     _call("attn_qk_norm_rope_bwd", index, q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),
           dq.data_ptr(), dk.data_ptr(), _pack18(*strides, *sq, *sk), _ptr(q_weight), _ptr(k_weight), bf16, _ptr(dwq), _ptr(dwk),
           *rot, 1 if interleaved else 0, B, N, Hq, Hkv, d, float(eps), _ptr(workspace), nbytes)
+    _changed(*given)
     return dq, dk, dwq, dwk
 
 

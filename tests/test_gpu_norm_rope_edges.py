@@ -33,3 +33,29 @@ def test_a_gradient_that_begins_off_a_16_byte_boundary():
     torch.cat([torch.zeros(3, device="cuda").bfloat16(), yq.flatten()]).backward(dy)
     for got, ref in zip(leaves, want):
         assert torch.equal(got.grad, ref)
+
+
+def test_a_tensor_written_in_place_is_not_used_by_a_backward():
+    """norm_rope saves q and k; a call that then writes to one of them makes the backward raise."""
+    q, k, pos, inv, wq, wk = _inputs(9, 4, 2, 64)
+    for which in (0, 1):
+        x = [t.clone().requires_grad_() for t in (q, k)]
+        out = attn.norm_rope(*x, pos, inv, wq, wk)
+        place = [None, None]
+        place[which] = x[which].detach()
+        attn.qk_norm_rope(q, k, pos, inv, wq, wk, q_out=place[0], k_out=place[1])
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            (out[0].sum() + out[1].sum()).backward()
+    x = [t.clone().requires_grad_() for t in (q, k)]
+    out = attn.norm_rope(*x, pos, inv, wq, wk)
+    attn.qk_norm_rope_bwd(q, k, q, k, pos, inv, wq, wk, dk=x[1].detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out[0].sum().backward()
+    # tensors that the call made itself, or only read, count as they did; inference tensors have no count
+    at = [t._version for t in (q, k, pos, inv, wq, wk)]
+    y = attn.qk_norm_rope(q, k, pos, inv, wq, wk)
+    assert [t._version for t in (q, k, pos, inv, wq, wk)] == at and y[0]._version == 0
+    with torch.inference_mode():
+        z = torch.empty_like(q)
+    attn.qk_norm_rope(q, k, pos, inv, wq, wk, q_out=z)
+    assert torch.equal(z, y[0])
