@@ -140,6 +140,13 @@ def _call(name, index, *args):
         _check(status, name)
 
 
+def _check_scratch(name, t, index):
+    """Scratch that a caller supplies: the kernels write its bytes from the first
+    to the last, which a strided view would share with others."""
+    if t is not None and (t.get_device() != index or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous tensor on the device of the inputs")
+
+
 def _changed(*tensors):
     """Tells autograd that a call wrote to the caller's own tensors (None: not
     given), so that a backward that saved one of them raises its usual error."""
@@ -223,6 +230,7 @@ def attn_fwd_partial(q, k, v, causal: bool = False, scale: float | None = None, 
         return out, lse
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check_scratch("workspace", workspace, q.get_device())
     st = lib().attn_fwd_partial_splitkv(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                         lse.data_ptr(), B, Hq, Hkv, Nq, Nkv, d, int(bool(causal)),
                                         float(scale), int(kv_tail), int(num_splits),
@@ -297,6 +305,7 @@ def attn_fwd_splitkv(q, k, v, causal: bool = False, scale: float | None = None,
     need = int(lib().attn_fwd_splitkv_workspace_size(B, Hq, Hkv, Nq, Nkv, d, int(num_splits)))
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check_scratch("workspace", workspace, q.get_device())
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
@@ -374,6 +383,7 @@ def attn_bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = 
     need = bwd_workspace_size(B, Hq, Hkv, Nq, Nkv, d)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check_scratch("workspace", workspace, q.get_device())
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
@@ -417,6 +427,7 @@ def attn_bwd_varlen(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seqle
     if workspace is None:
         need = int(lib().attn_bwd_varlen_workspace_size(n, Hq, int(max_seqlen_q), d))
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check_scratch("workspace", workspace, q.get_device())
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
@@ -531,6 +542,7 @@ def attn_fwd_q8(q, k, v, causal: bool = False, scale: float | None = None, works
     if workspace is None:
         workspace = torch.empty(q8_workspace_size(B, Hq, Hkv, Nq, Nkv, d), dtype=torch.uint8,
                                 device=q.device)
+    _check_scratch("workspace", workspace, q.get_device())
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
@@ -548,6 +560,7 @@ def attn_fwd_q8(q, k, v, causal: bool = False, scale: float | None = None, works
 def q8_prepass(q, k, v, workspace, qk_format: str = "int8"):
     """Run only the 8-bit prepass (K mean, scales, quantisation) into ``workspace``."""
     B, Hq, Hkv, Nq, Nkv, d = _shape_args(q, k, v)
+    _check_scratch("workspace", workspace, q.get_device())
     fn = lib().attn_q8_prepass if qk_format == "int8" else lib().attn_fp8_prepass
     st = fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hq, Hkv, Nq, Nkv, d,
             workspace.data_ptr(), workspace.numel(), _stream_handle(q.device))
@@ -574,6 +587,8 @@ def attn_fwd_host(q, k, v, causal: bool = False, scale: float | None = None, dev
     need = host_buffer_size(B, Hq, Hkv, Nq, Nkv, d)
     if dev_buf is None:
         dev_buf = torch.empty(need, dtype=torch.uint8, device="cuda")
+    if not dev_buf.is_cuda or not dev_buf.is_contiguous():
+        raise ValueError("dev_buf must be a contiguous CUDA tensor")
     if out is None:
         out = torch.empty_like(q)
     if lse is None:

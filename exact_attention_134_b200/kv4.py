@@ -21,7 +21,7 @@ from __future__ import annotations
 
 import math
 
-from . import _call, _changed, lib
+from . import _call, _changed, _check_scratch, lib
 
 
 def kv4_page_bytes(Hkv: int, d: int, page_size: int) -> int:
@@ -183,8 +183,8 @@ def attn_fwd_kv4(q, pool, page_table, seq_lens, cu_seqlens_q=None, max_seqlen_q:
         raise ValueError(f"lse must be a contiguous fp32 CUDA tensor {(Hq, total)} on the device of q")
     if workspace is None and max_pages * page_size > 512:  # shorter caches leave no partial results
         workspace = lse.new_empty((fwd_kv4_workspace_size(Hq, Hkv, max_seqlen_q, d) // 4,))
-    elif workspace is not None and workspace.get_device() != index:
-        raise ValueError("workspace must be on the device of q")
+    else:
+        _check_scratch("workspace", workspace, index)
     _call("attn_fwd_kv4", index, q.data_ptr(), pool.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
           _ptr(cu_seqlens_q), out.data_ptr(), lse.data_ptr(), n, max_pages, num_pages, page_size, int(max_seqlen_q),
           total, Hq, Hkv, d, 1 if causal else 0, float(scale), _ptr(workspace),

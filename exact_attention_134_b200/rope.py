@@ -14,7 +14,7 @@ from __future__ import annotations
 
 import struct
 
-from . import _call, _changed, lib
+from . import _call, _changed, _check_scratch, lib
 
 # arrays of long long and int as the C calls read them
 _pack12, _pack18 = struct.Struct("12q").pack, struct.Struct("18q").pack
@@ -193,8 +193,8 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, positions=None, inv_freq=None, q_weig
             dwq, dwk = torch.empty_like(q_weight), torch.empty_like(q_weight)
         if workspace is None:
             workspace = dwq.new_empty((lib().attn_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hkv, d) // 4,))
-        elif workspace.get_device() != index:
-            raise ValueError("workspace must be on the device of q")
+        else:
+            _check_scratch("workspace", workspace, index)
         nbytes = workspace.nbytes
     else:
         workspace = None

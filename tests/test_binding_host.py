@@ -1,4 +1,4 @@
-"""The host side of the norm with rotation (no GPU)."""
+"""The host side of the bindings (no GPU)."""
 import pytest
 import torch
 
@@ -17,3 +17,14 @@ def test_gradients_are_readable(make):
     r = rope._readable(t)
     assert torch.equal(r, t)
     assert r.stride(-1) == 1 and all(s % 8 == 0 for s in r.stride()[:-1]) and r.data_ptr() % 16 == 0
+
+
+def test_scratch_is_contiguous_and_on_the_device():
+    import exact_attention_134_b200 as attn
+    t = torch.empty(64, dtype=torch.uint8)
+    attn._check_scratch("workspace", None, 0)
+    attn._check_scratch("workspace", t, -1)                       # -1: the host, as get_device() has it
+    attn._check_scratch("workspace", t.view(torch.float32), -1)
+    for bad, index in ((t, 0), (t[::2], -1), (t.view(8, 8).T, -1), (t[:1].expand(64), -1)):
+        with pytest.raises(ValueError):
+            attn._check_scratch("workspace", bad, index)
