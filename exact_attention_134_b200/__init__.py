@@ -151,9 +151,9 @@ def _changed(*tensors):
     """Tells autograd that a call wrote to the caller's own tensors (None: not
     given), so that a backward that saved one of them raises its usual error."""
     import torch
-    for t in tensors:
-        if t is not None:
-            torch.autograd.graph.increment_version(t)
+    given = [t for t in tensors if t is not None]
+    if given:  # the raw call behind autograd.graph.increment_version(): a third of its time
+        torch._C._increment_version(given)
 
 
 def _shape_args(q, k, v):
