@@ -20,6 +20,7 @@ constexpr int kMaxDevices = 64;
 __device__ int g_status[4];
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+PFN_cuCtxGetCurrent_v4000 g_ctx_current = nullptr;
 std::once_flag g_encode_once;
 std::mutex g_dev_mutex;
 int* g_status_ptr[kMaxDevices] = {nullptr};
@@ -34,9 +35,12 @@ attn_status_t cuda_status(cudaError_t e) {
   return ATTN_ERR_CUDA;
 }
 
-void load_encode() {
+void load_driver() {
   void* fn = nullptr;
   cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &fn, 4000, cudaEnableDefault, &q) == cudaSuccess &&
+      q == cudaDriverEntryPointSuccess)
+    g_ctx_current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(fn);
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
                                        &q) == cudaSuccess &&
       q == cudaDriverEntryPointSuccess)
@@ -46,17 +50,15 @@ void load_encode() {
 // Per-device one-time set-up with that device current: the driver's tensor-map
 // encoder and the device address of the status word.
 int* device_status_ptr() {
-  std::call_once(g_encode_once, load_encode);
-  if (!g_encode) return nullptr;
+  std::call_once(g_encode_once, load_driver);
+  if (!g_encode || !g_ctx_current) return nullptr;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
   // A thread that made no CUDA call yet (autograd's, on its first node) has no
-  // current context, which the tensor-map encoder needs.
-  static thread_local int bound = -1;
-  if (bound != dev) {
-    if (cudaSetDevice(dev) != cudaSuccess) return nullptr;
-    bound = dev;
-  }
+  // current context, which the tensor-map encoder needs. One that the caller
+  // made current (its own, or one with a part of the SMs) stays.
+  CUcontext ctx = nullptr;
+  if ((g_ctx_current(&ctx) != CUDA_SUCCESS || !ctx) && cudaSetDevice(dev) != cudaSuccess) return nullptr;
   std::lock_guard<std::mutex> lock(g_dev_mutex);
   if (!g_status_ptr[dev]) {
     void* ptr = nullptr;

@@ -32,6 +32,9 @@
  *   - Ownership: the caller owns every buffer; device pointers must stay valid
  *     until the work queued on `stream` has finished. The library allocates no
  *     device memory. `stream` is a cudaStream_t (0 = legacy default stream).
+ *   - Context: work is queued in the calling thread's current context, which
+ *     stays current (a thread without one gets the device's primary context). A
+ *     process uses one context of a device, the first that it called with.
  *   - Asynchrony: work is queued on `stream`; nothing synchronises except
  *     where an entry point says so.
  *   - Errors: the return value is the only channel (nothing is printed, no
