@@ -426,7 +426,7 @@ attn_status_t kv4_pool_params(Kv4Pool* c, const void* pool, const int* page_tabl
   if (!cu && total % num_seqs) return ATTN_ERR_INVALID_ARG;
   if (page_size < kKv4Tile || page_size > 1024 || (page_size & (page_size - 1))) return ATTN_ERR_UNSUPPORTED;
   if (d != 64 && d != 96 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;
-  if (num_seqs > 65535 || Hkv > 65535 || (long long)max_pages * page_size > 0x7ffffff0LL) return ATTN_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || Hkv > 65535 || (long long)max_pages * page_size > kKv4MaxTokens) return ATTN_ERR_UNSUPPORTED;
   const uintptr_t ints = reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(seq_lens) |
                          reinterpret_cast<uintptr_t>(cu);
   if ((reinterpret_cast<uintptr_t>(pool) & 15u) || (ints & 3u)) return ATTN_ERR_ALIGNMENT;

@@ -28,6 +28,9 @@
 namespace attn_sm100 {
 
 constexpr int kKv4Tile = 16;  // tokens of a record
+// Most tokens that a page table may hold: positions, and a few records' worth
+// behind the last one, are computed in 32 bits.
+constexpr int kKv4MaxTokens = 0x7fff0000;
 
 __host__ __device__ constexpr int kv4_record_bytes(int d) { return 20 * d; }
 
@@ -45,8 +48,7 @@ struct Kv4Pool {
 
 // Tokens of sequence b in the cache, clamped to what its table row can hold.
 __device__ __forceinline__ int kv4_len(const Kv4Pool& c, int b) {
-  const long long most = (long long)c.max_pages << (c.tiles_log2 + 4);
-  return (int)min((long long)max(__ldg(c.seq_lens + b), 0), min(most, 0x7ffffff0LL));
+  return min(max(__ldg(c.seq_lens + b), 0), c.max_pages << (c.tiles_log2 + 4));
 }
 
 // First row and number of rows of sequence b, clamped to [0, total].

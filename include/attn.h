@@ -469,7 +469,8 @@ ATTN_API attn_status_t attn_qk_norm_rope_bwd(
  *   page_table  device, int32 [num_seqs][max_pages]: token j of sequence s is
  *               in page page_table[s][j / page_size]; entries behind a
  *               sequence's last token are not read. A page may belong to
- *               several sequences (a shared prefix)
+ *               several sequences (a shared prefix). max_pages * page_size is
+ *               at most 2^31 - 65536
  *   seq_lens    device, int32 [num_seqs]: tokens in the cache, those of the
  *               call included (values outside [0, max_pages * page_size] are
  *               clamped)

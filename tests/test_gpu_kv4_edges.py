@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import exact_attention_134_b200 as attn
+from oracle import kv4
 
 pytestmark = pytest.mark.gpu
 
@@ -18,6 +19,73 @@ def _gpu():
 
 def _ints(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _np(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def _pages_of(n, H, d, page, g):
+    """A pool of n full pages, and what each kv head's records of them stand for, page after page."""
+    k = torch.randn((n * page, H, d), generator=g) * (1 + 5 * (torch.rand(d, generator=g) < 0.1))
+    v = torch.randn((n * page, H, d), generator=g)
+    pool = torch.zeros((n, H, page // 16, 20 * d), dtype=torch.uint8, device="cuda")
+    attn.kv4_append(k.bfloat16().cuda(), v.bfloat16().cuda(), pool, _ints([list(range(n))]), _ints([n * page]))
+    return pool, [kv4.read_cache(pool.cpu().numpy(), list(range(n)), n * page, h) for h in range(H)]
+
+
+def _repeated_fp64(q, cache, counts, scale, chain):
+    """Attention of one row q [d] over the cache's tokens, token j counted counts[j] times:
+    (O, LSE, tol_O, tol_LSE). Tolerances as the oracle derives them for a few tokens, with the
+    roundings of `chain` additions one behind the other on top: 2^-24 of a sum of weights, 2^-23 of a
+    matrix instruction's accumulator, each of the size of all that is summed."""
+    x = scale * (cache["k"] @ q)
+    there = counts > 0
+    m = x[there].max()
+    p = counts * np.exp(np.minimum(x - m, 0.0))
+    l = p.sum()
+    w = p / l
+    O, L = w @ cache["v"], m + np.log(l)
+    size = scale * ((cache["ks"] * cache["kc"] + np.abs(cache["kl"])) @ np.abs(q))
+    ex = 2.0 ** -19 * size[there].max() + 2.0 ** -20
+    vs = cache["vs"][there].max()
+    ex += 2 * 2.0 ** -24 * np.log(2) * (8 + abs(np.log2(max(vs, 2.0 ** -126))))
+    codes, minima = w @ (cache["vs"] * cache["vc"]), w @ np.abs(cache["vl"])
+    tO = 2.0 ** -8 * np.abs(O) + (2.0 ** -11 + 2 * ex) * codes + (2.0 ** -15 + 2 * ex) * minima
+    tO += 15 * counts.sum() * 2.0 ** -32 * vs / l + chain * (2.0 ** -23 * (codes + minima) + 2.0 ** -24 * np.abs(O))
+    return O, L, tO, ex + 2.0 ** -22 * abs(L) + chain * 2.0 ** -24
+
+
+def _chain(tokens, ctas):
+    """Additions behind one another: two for each of a warp's records, then shuffles, warps and parts."""
+    return 2 * -(-tokens // (16 * 4 * ctas)) + 700
+
+
+def test_the_longest_page_tables():
+    """2^31 - 65536 tokens in 8 pages that repeat, one row a sequence; lengths beyond that are clamped."""
+    d, page, most = 64, 1024, 2 ** 31 - 65536
+    g = torch.Generator().manual_seed(21)
+    pool, (cache,) = _pages_of(8, 1, d, page, g)
+    table = torch.randint(0, 8, (2, most // page), generator=g).int()
+    lens = [most, 2 ** 31 - 1]
+    q = torch.randn((2, 2, d), generator=g).bfloat16()
+    o, lse = attn.attn_fwd_kv4(q.cuda(), pool, table.cuda(), _ints(lens), causal=True)
+    assert attn.get_status() == (0, 0)
+    for s in range(2):
+        counts = np.repeat(np.bincount(table[s].numpy(), minlength=8), page)
+        for h in range(2):
+            O, L, tO, tL = _repeated_fp64(_np(q[s, h]), cache, counts, 0.125, _chain(2 * most, 296))
+            assert abs(float(lse[h, s]) - L) <= tL
+            assert (np.abs(_np(o[s, h]) - O) <= tO).all()
+    # the last tokens read back, and written
+    last = int(table[0, -1])
+    k, v = attn.kv4_gather(pool, table.cuda(), _ints(lens), 6)
+    whole, _ = attn.kv4_gather(pool, _ints([[last]]), _ints([page]), 3)
+    assert torch.equal(k[:3], whole)
+    pool2 = pool.clone()
+    attn.kv4_append(k[:3] + 1, v[:3], pool, table[:1].cuda(), _ints(lens[:1]))
+    attn.kv4_append(k[:3] + 1, v[:3], pool2, _ints([[last]]), _ints([page]))
+    assert torch.equal(pool, pool2) and attn.get_status() == (0, 0)
 
 
 def test_tensors_that_calls_write_to_count_as_changed():
