@@ -37,6 +37,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxAxes = 4;
+// Most tokens: their number, rounded up to a block's, is computed in 32 bits.
+constexpr int kMaxTokens = 0x7fff0000;
 // Blocks of an SM and steps in a warp's ring. Large blocks and little in flight
 // keep a block's rows together in DRAM; more of either is slower once every
 // call's results are written back behind the next one's reads. Measured, one
@@ -422,7 +424,7 @@ attn_status_t rope_params(RopeParams* p, const void* const* tensors, int num_ten
   if (q_weight && !(isfinite(eps) && eps >= 0.0f)) return ATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 96 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;
   if (rotary_dim < 0 || rotary_dim > d || rotary_dim % 16) return ATTN_ERR_INVALID_ARG;
-  if (Hq > 65535 || Hkv > 65535 || (long long)B * N > 0x7ffffff0LL) return ATTN_ERR_UNSUPPORTED;
+  if (Hq > 65535 || Hkv > 65535 || (long long)B * N > kMaxTokens) return ATTN_ERR_UNSUPPORTED;
   *p = RopeParams();
   if (rotary_dim > 0) {
     if (!positions || !inv_freq || !sections || pos_axis_stride < 0 || pos_batch_stride < 0) return ATTN_ERR_INVALID_ARG;

@@ -414,7 +414,7 @@ ATTN_API attn_status_t attn_bwd_varlen(const void* q, const void* k, const void*
  *                  not rotated; 0: positions, inv_freq and sections are unused
  *   interleaved    0: pair i is channels (i, i + rotary_dim / 2); 1: (2i, 2i + 1)
  *   d              64, 96, 128 or 256
- * Packed sequences are B = 1 with N = total rows. B * N below 2^31 - 16. One
+ * Packed sequences are B = 1 with N = total rows. B * N is at most 2^31 - 65536. One
  * launch; allocates nothing.
  */
 ATTN_API attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,

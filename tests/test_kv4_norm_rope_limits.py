@@ -25,3 +25,19 @@ def test_tokens_of_a_page_table(lib, page, most):
     assert calls(most) == (3, 3, 3)
     assert calls(most + 1) == (2, 2, 2)
     assert calls((2 ** 31 - 16) // page) == (2, 2, 2)  # 2^31 - 16 tokens: 32 behind them pass 2^31
+
+
+def test_tokens_of_a_norm_rope_call(lib):
+    """2^31 - 65536 tokens are taken (and the tensors' alignment is looked at next), one more is not."""
+    import ctypes
+
+    def calls(n):
+        def s(k):
+            return (ctypes.c_longlong * (3 * k))(*[64] * (3 * k))
+        return (lib.attn_qk_norm_rope(P + 8, P, P, P, s(4), None, None, 0, None, 0, 0, None, None, 0, 0, 0, 1, n, 1, 1,
+                                      64, 0.0, None),
+                lib.attn_qk_norm_rope_bwd(P + 8, P, P, P, P, P, s(6), None, None, 0, None, None, None, 0, 0, None, None,
+                                          0, 0, 0, 1, n, 1, 1, 64, 0.0, None, 0, None))
+    assert calls(2 ** 31 - 65536) == (3, 3)
+    assert calls(2 ** 31 - 65535) == (2, 2)
+    assert calls(2 ** 31 - 17) == (2, 2)  # rounded up to 64 tokens this passes 2^31
