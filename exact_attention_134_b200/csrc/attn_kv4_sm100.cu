@@ -438,9 +438,12 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
       top = max(top, __shfl_xor_sync(kFull, top, 1));
       top = max(top, __shfl_xor_sync(kFull, top, 2));
       // the row's largest value into [2^13, 2^14): a sixteenth of it, for the
-      // codes that stand 4 bits up, still is a normal number down to 2^-24 of it
-      const int k = min(max(13 - ((int)(top >> 7) - 127), -90), 100);
-      const float up = __uint_as_float((uint32_t)(k + 127) << 23);
+      // codes that stand 4 bits up, still is a normal number down to 2^-24 of
+      // it. Small rows take the largest power there is; large ones stop at
+      // 2^-90, so that its inverse times 2^24 stays finite with the scale: from
+      // 2^106 on (13 - 105 is -92, where fp16 still holds it) a row gets NaN
+      const int want = 13 - ((int)(top >> 7) - 127), k = min(max(want, -90), 127);
+      const float up = want < -92 ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)(k + 127) << 23);
       float mine = 0.0f, other = 0.0f;  // the sums over groups t4 and t4 + 4
 #pragma unroll
       for (int gr = 0; gr < G; ++gr) {

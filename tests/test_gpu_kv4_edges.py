@@ -88,6 +88,42 @@ def test_the_longest_page_tables():
     assert torch.equal(pool, pool2) and attn.get_status() == (0, 0)
 
 
+@pytest.mark.parametrize("Hq", [3, 8, 14])
+@pytest.mark.parametrize("up", [-120, -112, 0, 90, 102])
+def test_queries_of_every_size(Hq, up):
+    """Queries and keys of inverse sizes: the same scores; rows whose largest value is 2^106 or more are NaN."""
+    g = torch.Generator().manual_seed(22)
+    n, d = 70, 128
+    k = torch.randn((n, 1, d), generator=g) * 2.0 ** -up
+    v = torch.randn((n, 1, d), generator=g)
+    q = torch.randn((1, Hq, d), generator=g).clamp(-7, 7) * 2.0 ** up
+    pool = torch.zeros((5, 1, 1, 20 * d), dtype=torch.uint8, device="cuda")
+    args = pool, _ints([[3, 0, 4, 1, 2]]), _ints([n])
+    attn.kv4_append(k.bfloat16().cuda(), v.bfloat16().cuda(), *args)
+    cache = kv4.read_cache(pool.cpu().numpy(), [3, 0, 4, 1, 2], n, 0)
+    q = q.bfloat16()
+    O, L, tO, tL = kv4.attention_kv4_fp64(_np(q), [cache], True, d ** -0.5)
+    o, lse = attn.attn_fwd_kv4(q.cuda(), *args, causal=True)
+    assert (np.abs(_np(o) - O) <= tO).all() and (np.abs(_np(lse).T - L) <= tL).all()
+    for large in (-2.0 ** 106, 2.0 ** 127, float("inf"), float("-inf"), float("nan")):
+        bad = q.clone()
+        bad[0, 1] = 0
+        bad[0, 1, 77] = large
+        o2, lse2 = attn.attn_fwd_kv4(bad.cuda(), *args, causal=True)
+        assert o2[0, 1].isnan().all() and lse2[1].isnan().all()
+        rest = [h for h in range(Hq) if h != 1]
+        assert (np.abs(_np(o2) - O) <= tO)[:, rest].all() and (np.abs(_np(lse2).T - L) <= tL)[:, rest].all()
+    edge = torch.zeros_like(q)  # the largest allowed: finite
+    edge[0, 0, 5] = -255 * 2.0 ** 98
+    small = torch.zeros((1, 1, 1, 20 * d), dtype=torch.uint8, device="cuda")
+    one = small, _ints([[0]]), _ints([1])
+    attn.kv4_append((torch.randn((1, 1, d), generator=g) * 2.0 ** -100).bfloat16().cuda(), v[:1].bfloat16().cuda(), *one)
+    o3, lse3 = attn.attn_fwd_kv4(edge.cuda(), *one)
+    O, L, tO, tL = kv4.attention_kv4_fp64(_np(edge), [kv4.read_cache(small.cpu().numpy(), [0], 1, 0)], True, d ** -0.5)
+    assert (np.abs(_np(o3) - O) <= tO).all() and (np.abs(_np(lse3).T - L) <= tL).all()
+    assert attn.get_status() == (0, 0)
+
+
 def test_tensors_that_calls_write_to_count_as_changed():
     """What autograd goes by when a tensor that it saved was written to."""
     pool = attn.kv4_alloc(4, 2, 64, 16)
