@@ -19,8 +19,11 @@
 // dequantised register straight into the instruction; tcgen05 would need them
 // written to shared or tensor memory first, and its accumulators read back for
 // the scale of every group. Q is scaled by a power of two a row into fp16's
-// range; P^T = p * s is fp16 as well (rounded once: 2^-12), against a reference
-// that follows the row's maximum and the keys' scales: p * s < 2^15. The minima
+// range; P^T = p * s is fp16 as well, against a reference that follows the row's
+// maximum and the keys' scales: 2^7 <= its largest < 2^15. It is rounded once (by
+// 2^-11 at most, by 2^-25 below 2^-14, which is 2^-21 of the largest): a second
+// piece would double the output's instructions, and against 64 bits the batch
+// below is off by 0.00173 where 0.00166 are the result's own rounding. The minima
 // take p in two bf16 pieces (16 bits): they cancel against the codes' part.
 //
 // Work. A unit is a pair of records of one block of query rows (4, 8 or 16 of a

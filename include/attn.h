@@ -546,8 +546,10 @@ ATTN_API attn_status_t attn_kv4_copy_pages(void* pool, int num_layers, int num_p
  * Any number of query rows is computed, 4, 8 or 16 (row, head) pairs of a kv head
  * in one pass over its cache; for long chunks attn_kv4_gather and
  * attn_fwd_varlen are faster. |q| below 2^106 (a row with a larger value gets
- * NaN); |v| up to 2^64; a token's groups whose scale is below 2^-20 of its
- * largest lose precision. One launch where page_table holds
+ * NaN); |v| up to 2^64. A token's weight times a group's scale is held in fp16
+ * against the largest such product of the row, over all tokens and groups
+ * (where scales below 2^-64 count as 2^-64): products below 2^-21 of it can lose
+ * bits, and below 2^-32 the group can count as its minimum. One launch where page_table holds
  * at most 512 tokens a sequence (1024 with many sequences), else two (attention,
  * merge of what was split); allocates nothing; deterministic.
  */

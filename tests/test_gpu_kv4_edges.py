@@ -124,6 +124,38 @@ def test_queries_of_every_size(Hq, up):
     assert attn.get_status() == (0, 0)
 
 
+@pytest.mark.parametrize("Hq", [4, 8, 13])
+@pytest.mark.parametrize("what", ["one large token", "one large group", "large first", "2^-75", "2^-90", "2^-110"])
+def test_values_whose_scales_lie_far_apart(Hq, what):
+    """What the fp16 range of weights times scales leaves: 2^-32 of the row's largest product, over all
+    tokens and groups, where scales below 2^-64 count as 2^-64."""
+    g = torch.Generator().manual_seed(23)
+    n, d = 150, 128
+    k, v = torch.randn((n, 1, d), generator=g), torch.randn((n, 1, d), generator=g)
+    if what == "one large token":
+        v[77] *= 2.0 ** 24
+    elif what == "one large group":
+        v[77, :, 32:64] *= 2.0 ** 30
+    elif what == "large first":
+        v[0] *= 2.0 ** 40
+        k[0] = 0
+    else:
+        v *= 2.0 ** int(what[2:])
+    q = torch.randn((1, Hq, d), generator=g).bfloat16()
+    pool = torch.zeros((10, 1, 1, 20 * d), dtype=torch.uint8, device="cuda")
+    args = pool, _ints([list(range(10))]), _ints([n])
+    attn.kv4_append(k.bfloat16().cuda(), v.bfloat16().cuda(), *args)
+    o, lse = attn.attn_fwd_kv4(q.cuda(), *args, causal=True)
+    assert attn.get_status() == (0, 0)
+    cache = kv4.read_cache(pool.cpu().numpy(), list(range(10)), n, 0)
+    # the oracle's bound has the largest scale that there is; 2^-64 stands for a smaller one
+    O, L, tO, tL = kv4.attention_kv4_fp64(_np(q), [cache], True, d ** -0.5)
+    x = d ** -0.5 * (cache["k"] @ _np(q)[0].T)
+    low = 15 * n * 2.0 ** -32 * max(0.0, 2.0 ** -64 - cache["vs"].max()) / np.exp(x - x.max(0)).sum(0)
+    assert (np.abs(_np(o) - O) <= tO + low[None, :, None]).all()
+    assert (np.abs(_np(lse).T - L) <= tL).all()
+
+
 def test_tensors_that_calls_write_to_count_as_changed():
     """What autograd goes by when a tensor that it saved was written to."""
     pool = attn.kv4_alloc(4, 2, 64, 16)
