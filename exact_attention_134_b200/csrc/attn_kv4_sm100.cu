@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, COLS>::kWarps * 32, Kv4Cfg<D, COLS>:
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[nt][e] = 0.0f;
-        // the minima of key g8 (+ 8) and group t4: once for each of two pieces of the sums
+        // the minima of key g8 (+ 8) and group t4: once for each piece of the sums (three, and a zero)
 #pragma unroll
         for (int i = 0; i < Q; ++i)
 #pragma unroll

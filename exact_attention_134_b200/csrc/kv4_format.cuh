@@ -25,6 +25,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "../../include/attn.h"
+
 namespace attn_sm100 {
 
 constexpr int kKv4Tile = 16;  // tokens of a record
@@ -123,10 +125,9 @@ __device__ __forceinline__ size_t kv4_record(const Kv4Pool& c, int page, int h, 
   return ((((size_t)page * c.Hkv + h) << c.tiles_log2) + tile) * (size_t)kv4_record_bytes(d);
 }
 
-// Records a page id outside the pool in the device status word (2 =
-// an argument on the device; ATTN_ERR_INVALID_ARG), first failure only.
+// Records a page id outside the pool in the device status word, if it is the first failure there.
 __device__ __forceinline__ void kv4_bad_page(int* status, int where) {
-  if (atomicCAS(status, 0, 1) == 0) status[1] = where;
+  if (atomicCAS(status, 0, ATTN_ERR_INVALID_ARG) == 0) status[1] = where;
 }
 
 }  // namespace attn_sm100
