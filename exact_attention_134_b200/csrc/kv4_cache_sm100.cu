@@ -502,6 +502,7 @@ attn_status_t attn_kv4_gather(const void* pool, const int* page_table, const int
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15u) return ATTN_ERR_ALIGNMENT;
   const CacheGrid g = cache_grid(p.c, d);
   if (g.threads == 0) return ATTN_ERR_UNSUPPORTED;
+  if (k == v) return ATTN_ERR_INVALID_ARG;
   p.status = device_status_word();
   if (!p.status) return ATTN_ERR_CUDA;
   p.y[0] = static_cast<uint16_t*>(k);

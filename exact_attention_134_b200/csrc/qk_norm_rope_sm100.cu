@@ -408,6 +408,11 @@ bool apart(const void* x, const long long* xs, const void* y, const long long* y
   return x != y || (xs[0] == ys[0] && xs[1] == ys[1] && xs[2] == ys[2]);
 }
 
+// Whether the two results are two tensors, and neither is what the other one is made of.
+bool uncrossed(const void* const* x, const void* const* y) {
+  return y[0] != y[1] && y[0] != x[1] && y[1] != x[0];
+}
+
 // The checks and parameters that both directions share. tensors: q, k, then
 // for each further pair as the caller lists them (strides in the same order).
 attn_status_t rope_params(RopeParams* p, const void* const* tensors, int num_tensors, const long long* strides,
@@ -487,7 +492,8 @@ attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q_out, void*
       rope_params(&p, t, 4, strides, q_weight, k_weight, weight_bf16, positions, pos_axis_stride, pos_batch_stride,
                   inv_freq, sections, num_axes, rotary_dim, interleaved, B, N, Hq, Hkv, d, eps);
   if (s != ATTN_OK) return s;
-  if (!apart(q, strides, q_out, strides + 6) || !apart(k, strides + 3, k_out, strides + 9)) return ATTN_ERR_INVALID_ARG;
+  if (!apart(q, strides, q_out, strides + 6) || !apart(k, strides + 3, k_out, strides + 9) || !uncrossed(t, t + 2))
+    return ATTN_ERR_INVALID_ARG;
   p.x[0] = static_cast<const uint16_t*>(q);
   p.x[1] = static_cast<const uint16_t*>(k);
   p.y[0] = static_cast<uint16_t*>(q_out);
@@ -519,7 +525,10 @@ attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq
       rope_params(&p, t, 6, strides, q_weight, k_weight, weight_bf16, positions, pos_axis_stride, pos_batch_stride,
                   inv_freq, sections, num_axes, rotary_dim, interleaved, B, N, Hq, Hkv, d, eps);
   if (s != ATTN_OK) return s;
-  if (!apart(dq_out, strides + 6, dq, strides + 12) || !apart(dk_out, strides + 9, dk, strides + 15))
+  if (!apart(dq_out, strides + 6, dq, strides + 12) || !apart(dk_out, strides + 9, dk, strides + 15) ||
+      !uncrossed(t + 2, t + 4))
+    return ATTN_ERR_INVALID_ARG;
+  if (q_weight && (!apart(q, strides, dq, strides + 12) || !apart(k, strides + 3, dk, strides + 15) || !uncrossed(t, t + 4)))
     return ATTN_ERR_INVALID_ARG;
   if (q_weight) {
     if (!dq_weight || !dk_weight) return ATTN_ERR_INVALID_ARG;

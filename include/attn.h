@@ -397,8 +397,9 @@ ATTN_API attn_status_t attn_bwd_varlen(const void* q, const void* k, const void*
  *   q, k           device, bf16, rows of d values at
  *                  b * strides[0] + h * strides[1] + n * strides[2] (read)
  *   q_out, k_out   device, bf16, the same with their own strides (written);
- *                  each may be q or k itself with the same strides, and
- *                  overlaps no other tensor of the call otherwise
+ *                  q_out may be q itself and k_out k, with the same strides;
+ *                  they overlap no other tensor of the call otherwise (the
+ *                  same address for two of them is refused)
  *   strides        host, 3 (batch, head, token) each for q, k, q_out, k_out, in
  *                  elements, >= 0 and multiples of 8
  *   q_weight, k_weight  device [d], fp32, or bf16 with weight_bf16 = 1; both
@@ -433,8 +434,9 @@ ATTN_API attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q_o
  *     dw = sum over batch, heads and tokens of dn * xhat.
  *   q, k             the forward's inputs (not read without a norm)
  *   dq_out, dk_out   device, bf16, gradients of q_out, k_out (read)
- *   dq, dk           device, bf16, gradients of q, k (written; each may be
- *                    dq_out or dk_out itself with the same strides)
+ *   dq, dk           device, bf16, gradients of q, k (written; dq may be dq_out
+ *                    itself and dk dk_out, with the same strides; they overlap
+ *                    no other tensor of the call otherwise)
  *   strides          host, 3 each for q, k, dq_out, dk_out, dq, dk
  *   dq_weight, dk_weight  device, fp32 [d] (written; unused without a norm)
  *   workspace        device, attn_qk_norm_rope_bwd_workspace_size() bytes,
@@ -502,8 +504,8 @@ ATTN_API attn_status_t attn_kv4_append(const void* k, const void* v, long long k
 
 /*
  * attn_kv4_gather — reads tokens back as bf16, packed as attn_fwd_varlen takes
- * them: k, v [total, Hkv, d] (written; rows that no sequence owns are left as
- * they were, rows at a token below 0 or on a bad page are 0). With
+ * them: k, v [total, Hkv, d] (written, two tensors; rows that no sequence owns
+ * are left as they were, rows at a token below 0 or on a bad page are 0). With
  * cu_seqlens = the offsets of seq_lens this is the whole context, for the
  * attention of a chunk of many query tokens. One launch; allocates nothing.
  */

@@ -41,3 +41,25 @@ def test_tokens_of_a_norm_rope_call(lib):
     assert calls(2 ** 31 - 65536) == (3, 3)
     assert calls(2 ** 31 - 65535) == (2, 2)
     assert calls(2 ** 31 - 17) == (2, 2)  # rounded up to 64 tokens this passes 2^31
+
+
+def test_results_that_are_one_tensor_or_the_other_ones_source(lib):
+    """q_out and k_out (dq and dk) at one address, or one of them where the other one is read from:
+    blocks of the two would write over what they read. Refused, as every pair is."""
+    import ctypes
+    q, k, a, b, c, d, w = (P + 0x1000 * i for i in range(7))
+
+    def fwd(qo, ko):
+        s = (ctypes.c_longlong * 12)(*[64] * 12)
+        return lib.attn_qk_norm_rope(q, k, qo, ko, s, w, w, 0, None, 0, 0, None, None, 0, 0, 0, 1, 9, 1, 1, 64, 0.0, None)
+
+    def bwd(dq, dk, weight=w):
+        s = (ctypes.c_longlong * 18)(*[64] * 18)
+        need = lib.attn_qk_norm_rope_bwd_workspace_size(1, 9, 1, 1, 64)
+        return lib.attn_qk_norm_rope_bwd(q, k, a, b, dq, dk, s, weight, weight, 0, w, w, None, 0, 0, None, None, 0, 0, 0, 1,
+                                         9, 1, 1, 64, 0.0, None, need, None)  # no workspace: 6 is what comes next
+    assert fwd(a, a) == fwd(k, b) == fwd(a, q) == fwd(k, q) == 1
+    assert bwd(c, c) == bwd(b, d) == bwd(c, a) == bwd(b, a) == 1
+    assert bwd(k, d) == bwd(c, q) == 1
+    assert bwd(c, d) == bwd(a, b) == bwd(a, d) == bwd(q, k) == 6
+    assert lib.attn_kv4_gather(P, P, P, P, 1, 8, 8, 16, 1, 1, 64, a, a, None) == 1
