@@ -393,7 +393,9 @@ ATTN_API attn_status_t attn_bwd_varlen(const void* q, const void* k, const void*
  *     pair i = (a, b) of n:  a' = a cos t - b sin t,  b' = a sin t + b cos t,
  *     t = position[axis of i] * inv_freq[i]
  * computed in fp32 (the angle in fp64, reduced to a fraction of a turn) and
- * rounded once.
+ * rounded once. The sum of x^2 is fp32's as well: |x| below 2^59 (a row with a
+ * larger value can come out as 0), and where mean(x^2) is below 2^-100 it counts
+ * beside eps only roughly.
  *   q, k           device, bf16, rows of d values at
  *                  b * strides[0] + h * strides[1] + n * strides[2] (read)
  *   q_out, k_out   device, bf16, the same with their own strides (written);

@@ -59,3 +59,20 @@ def test_a_tensor_written_in_place_is_not_used_by_a_backward():
         z = torch.empty_like(q)
     attn.qk_norm_rope(q, k, pos, inv, wq, wk, q_out=z)
     assert torch.equal(z, y[0])
+
+
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+def test_the_largest_rows(d):
+    """Rows of values just below 2^59: the sum of their squares is still finite."""
+    q, k, pos, inv, wq, wk = _inputs(33, 2, 1, d)
+    x = [(torch.sign(t.float()) * 2.0 ** 58 * 1.9921875).bfloat16() for t in (q, k)]
+    y = attn.qk_norm_rope(*x, q_weight=wq, k_weight=wk)
+    for got, s, w in zip(y, x, (wq, wk)):
+        want = torch.sign(s.double()) * w.double()
+        assert ((got.double() - want).abs() <= (torch.finfo(torch.bfloat16).eps / 2 + 2.0 ** -18) * want.abs()).all()
+    dq, dk, dwq, dwk = attn.qk_norm_rope_bwd(*x, q, k, q_weight=wq, k_weight=wk)
+    # dw = sum over rows of dy * sign(x); fp32 sums of fewer than 2^7 terms
+    for dw, s, dy in ((dwq, x[0], q), (dwk, x[1], k)):
+        terms = dy.double() * torch.sign(s.double())
+        assert ((dw.double() - terms.sum((0, 1))).abs() <= 2.0 ** -17 * terms.abs().sum((0, 1))).all()
+    assert dq.isfinite().all() and dk.isfinite().all()
