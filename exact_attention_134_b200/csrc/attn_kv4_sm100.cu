@@ -23,7 +23,7 @@
 // maximum and the keys' scales: 2^7 <= its largest < 2^15. It is rounded once (by
 // 2^-11 at most, by 2^-25 below 2^-14, which is 2^-21 of the largest): a second
 // piece would double the output's instructions, and against 64 bits the batch
-// below is off by 0.00173 where 0.00166 are the result's own rounding. The minima
+// below is off by 0.00171 where 0.00165 are the result's own rounding. The minima
 // take p in two bf16 pieces (16 bits): they cancel against the codes' part.
 //
 // Work. A unit is a pair of records of one block of query rows (4, 8 or 16 of a
@@ -39,13 +39,14 @@
 // 520 warp instructions a pair of records at d = 128 (5120 bytes: 222 clocks of
 // an SM's share of the memory rate, 888 issue slots). Measured (B200, one query
 // row of 32 / 8 heads, launches in a graph): 64 sequences of 4096 .. 8192 tokens
-// 98 us, 5.2 TB/s; one of 131072 44 us. From the first kernel on: a record a
-// step with minima on the FMA pipe 162 us; two records a step and minima by a
-// matrix instruction 137; four warps and three CTAs an SM instead of eight and
-// two 125; up to four rows against both records at once 112; query operands in
-// shared memory 110; the fourth operand by subtraction, weights moved instead of
-// masked 102. Five tiles of columns a warp, or a warp a tile on a shared ring,
-// were no faster for 40 rows (41 and 53 us against 37 with passes of 16): the
+// 96 us, 5.3 TB/s (87 with the arithmetic of the records left out); one of 131072
+// 42 us (37). From the first kernel on, 64 sequences: a record a step with minima
+// on the FMA pipe 162 us; two records a step and minima by a matrix instruction
+// 137; four warps and three CTAs an SM instead of eight and two 125; up to four
+// rows against both records at once 112; query operands in shared memory 110;
+// the fourth operand by subtraction, weights moved instead of masked 102. Five
+// tiles of columns a warp, or a warp a tile on a shared ring, were no faster for
+// 40 rows (41 and 53 us against 37 with passes of 16): the
 // scales and weights of a row cost more than its share of the codes.
 #include <cuda_runtime.h>
 #include <math.h>
@@ -231,7 +232,9 @@ struct Segment {
 };
 
 // Finds the segment of the list that holds unit `u` (the whole warp takes
-// part). False if the list ends before it.
+// part). False if the list ends before it. Every CTA walks over all sequences,
+// here and for their total: of 16384 sequences of 32 .. 64 tokens (530 us, one kv
+// head) nothing of it shows, of 65535 some 340 of 2463 us.
 template <int COLS>
 __device__ __forceinline__ bool find_segment(const Kv4Params& p, long long u, Segment& g) {
   const int lane = threadIdx.x & 31;
