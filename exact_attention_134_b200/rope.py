@@ -248,6 +248,8 @@ def _autograd_fn():
 def norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6,
               sections=None, interleaved: bool = False):
     """Differentiable qk_norm_rope (gradients of q, k, q_weight and k_weight):
-    forward attn_qk_norm_rope, backward attn_qk_norm_rope_bwd. Same arguments."""
+    forward attn_qk_norm_rope, backward attn_qk_norm_rope_bwd. Same arguments.
+    A step with its backward can be captured as torch asks for it: after warm-up
+    on a side stream, with no eager graph of the same leaves alive."""
     return _autograd_fn().apply(q, k, positions, inv_freq, q_weight, k_weight, float(eps),
                                 None if sections is None else tuple(sections), bool(interleaved))

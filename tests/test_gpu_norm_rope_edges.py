@@ -76,3 +76,44 @@ def test_the_largest_rows(d):
         terms = dy.double() * torch.sign(s.double())
         assert ((dw.double() - terms.sum((0, 1))).abs() <= 2.0 ** -17 * terms.abs().sum((0, 1))).all()
     assert dq.isfinite().all() and dk.isfinite().all()
+
+
+def test_a_captured_training_step():
+    """Norm and rotation, attention and their backward in one graph, captured as torch asks for it: after
+    warm-up on a side stream, with no eager graph of the leaves alive. Replayed with other inputs."""
+    N, d = 150, 64
+    q0, k0, pos, inv, wq0, wk0 = _inputs(N, 4, 2, d, seed=5)
+    q0, k0 = (t.transpose(0, 1)[None].contiguous() for t in (q0, k0))
+    v0, dout = torch.randn_like(k0), torch.randn_like(q0)
+    leaves = [t.clone().requires_grad_() for t in (q0, k0, v0, wq0, wk0)]
+
+    def step(q, k, v, wq, wk):
+        yq, yk = attn.norm_rope(q, k, pos, inv, wq, wk)
+        attn.attention(yq, yk, v, causal=True).backward(dout)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            step(*leaves)
+            for t in leaves:
+                t.grad = None
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*leaves)
+    for seed in (6, 7):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        with torch.no_grad():
+            for t in leaves:
+                t.copy_(torch.randn(t.shape, device="cuda", generator=g))
+            dout.copy_(torch.randn(dout.shape, device="cuda", generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        fresh = [t.detach().clone().requires_grad_() for t in leaves]
+        step(*fresh)
+        # dQ of attention is summed by atomics, in any order, in fp32: one step of bf16 here and there
+        for a, b in zip(leaves, fresh):
+            err = (a.grad.double() - b.grad.double()).norm() / b.grad.double().norm()
+            assert err <= torch.finfo(torch.bfloat16).eps / 2, err.item()
+    assert attn.get_status() == (0, 0)
